@@ -399,6 +399,185 @@ LQ_API lq_status lq_device_status(lq_handle h, void *stream);
  * Source: none. */
 LQ_API lq_status lq_state_destroy(lq_handle h);
 
+/* ------------------------------------------------------------------------
+ * Stateless operators that stand beside the decode path.  They take no
+ * handle, keep nothing between calls, allocate nothing and never
+ * synchronize; a call may be captured into a CUDA graph.  `stream` belongs to
+ * the calling thread's current device, and every pointer to memory that this
+ * device can reach.  Two calls may run at once on different streams as long
+ * as neither writes what the other reads or writes (workspaces and
+ * checkpoints included).  Outputs must not overlap inputs or other outputs
+ * except where a field says so.  They report no device errors: masks,
+ * lengths and values outside the stated ranges are handled as stated here.
+ * Each is the same from run to run on the same inputs (no atomics).
+ * ---------------------------------------------------------------------- */
+
+/* Element strides of a [token][sequence][head][...] tensor; the innermost
+ * channels (where the tensor has them) are contiguous. */
+typedef struct lq_strides {
+    int64_t token;
+    int64_t seq;
+    int64_t head;
+} lq_strides;
+
+/*
+ * A gated linear recurrence over vector states: for every sequence, head and
+ * channel, with alpha_t = exp(g_t),
+ *     h_t = alpha_t h_{t-1} + beta_t v_t,     out_t = h_t.
+ * It is the rule of the matrix states above without keys: the state of a head
+ * is one vector of d channels.  States, gates and sums are FP32.
+ */
+typedef struct lq_scan_config {
+    int32_t batch;        /* sequences, >= 1                                     */
+    int32_t heads;        /* heads per sequence, >= 1; batch * heads <= 2^24     */
+    int32_t d;            /* channels of a head, 1..256                          */
+    int32_t gate;         /* LQ_GATE_SCALAR (g [.]) or LQ_GATE_CHANNEL (g [.][d])*/
+    int32_t in_dtype;     /* v and grad_v: LQ_DTYPE_*                            */
+    int32_t out_dtype;    /* out and grad_out: LQ_DTYPE_*                        */
+} lq_scan_config;
+
+typedef struct lq_scan_args {
+    int32_t n_tokens;          /* T, >= 0                                         */
+    int32_t reserved;          /* must be 0                                       */
+    const void *v;             /* in_dtype [T][batch][heads][d], any strides      */
+    const float *g;            /* f32 [T][batch][heads] or [..][d]: log alpha,
+                                  <= 0 in ordinary use (-inf empties the state)   */
+    const float *beta;         /* f32 [T][batch][heads]; NULL: 1                  */
+    const float *h0;           /* f32 [batch][heads][d]: start; NULL: zero        */
+    const int32_t *lengths;    /* int32 [batch]: tokens of each sequence, clamped
+                                  to 0..T; NULL: T.  Tokens past a length are
+                                  neither read nor written                        */
+    void *out;                 /* out_dtype [T][batch][heads][d]; NULL: not wanted*/
+    float *h_last;             /* f32 [batch][heads][d]: state after the last
+                                  token (h0 where there is none); may be h0;
+                                  NULL: not wanted                                */
+    float *checkpoints;        /* lq_gated_scan_checkpoint_bytes() for the
+                                  backward pass; NULL in lq_gated_scan(): not
+                                  wanted                                          */
+    lq_strides v_stride, g_stride, beta_stride, out_stride;
+} lq_scan_args;
+
+/* Gradients; a NULL output is not computed. */
+typedef struct lq_scan_grads {
+    const void *grad_out;      /* out_dtype [T][batch][heads][d]; NULL: zero      */
+    const float *grad_last;    /* f32 [batch][heads][d]; NULL: zero               */
+    void *grad_v;              /* in_dtype, as v                                  */
+    float *grad_g;             /* f32, as g (scalar gate: summed over channels)   */
+    float *grad_beta;          /* f32, as beta; NULL when beta is NULL            */
+    float *grad_h0;            /* f32 [batch][heads][d]; may be grad_last         */
+    lq_strides grad_out_stride, grad_v_stride, grad_g_stride, grad_beta_stride;
+} lq_scan_grads;
+
+/* Bytes of the checkpoints of n_tokens tokens (0 for an invalid config or a
+ * negative count).  Source: none (memory sizing). */
+LQ_API size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t n_tokens);
+
+/*
+ * The recurrence over n_tokens tokens of every sequence: a prompt, a training
+ * sequence, or (n_tokens = 1) one decode token.  Long sequences are split over
+ * the device.  With `checkpoints` it leaves there what the backward pass needs
+ * besides the inputs.
+ * Errors: LQ_ERR_INVALID_ARG for a bad config field, a NULL v or g with
+ * n_tokens > 0, a negative n_tokens, a pointer not aligned to its element or
+ * an output dimension of stride 0.
+ * Source: [abs] (the gated linear recurrence that GDN and KDA build on; the
+ * pages describe no vector-state layer).
+ */
+LQ_API lq_status lq_gated_scan(const lq_scan_config *cfg, const lq_scan_args *args, void *stream);
+
+/*
+ * The gradients of lq_gated_scan() given those of out and h_last.  `args` as
+ * in the forward call (its out, h_last and h0 are not used), `checkpoints`
+ * filled by it.  With D_t the gradient of h_t by all that follows:
+ *     D_t = grad_out_t + alpha_{t+1} D_{t+1}   (last token: + grad_last)
+ *     grad_v_t = beta_t D_t        grad_beta_t = sum_c v_t D_t
+ *     grad_g_t = alpha_t h_{t-1} D_t           grad_h0 = alpha_0 D_0.
+ * Errors: as lq_gated_scan(), and LQ_ERR_INVALID_ARG for NULL grads or
+ * checkpoints, or a grad_beta without beta.
+ * Source: none (the derivative of the recurrence).
+ */
+LQ_API lq_status lq_gated_scan_backward(const lq_scan_config *cfg, const lq_scan_args *args,
+                                        const lq_scan_grads *grads, void *stream);
+
+enum {
+    LQ_NORM_L2 = 0,   /* x / sqrt(sum x^2 + eps): q and k of a gated delta-rule layer */
+    LQ_NORM_RMS = 1   /* x / sqrt(mean x^2 + eps)                                     */
+};
+enum {
+    LQ_PAIRS_HALF = 0,        /* channel i turns with i + rot_dim / 2 */
+    LQ_PAIRS_NEIGHBOURS = 1   /* channel 2 i turns with 2 i + 1       */
+};
+
+/*
+ * Norms of queries and keys for each head with the position rotation in the
+ * same pass: what makes a projection's q and k the ones that the decode and
+ * prefill calls take.  For every token and head
+ *     u = x w / sqrt(sum x^2 (or mean x^2) + eps),
+ * then the first rot_dim channels turn in pairs by the angles
+ * theta_i = position * inv_freq[i],
+ *     (u_a, u_b) -> (u_a cos theta_i - u_b sin theta_i, u_b cos theta_i + u_a sin theta_i),
+ * and q is multiplied by q_scale.  FP32 inside, rounded once; the angles are
+ * formed in FP64, so positions up to 2^31 - 1 keep FP32 accuracy.
+ */
+typedef struct lq_qk_norm_config {
+    int32_t heads_q;      /* query heads, >= 1                                   */
+    int32_t heads_k;      /* key heads, >= 0 (0: queries only)                   */
+    int32_t d;            /* channels of a head, 1..256                          */
+    int32_t norm;         /* LQ_NORM_*                                           */
+    int32_t rot_dim;      /* rotated channels, even, 0..d (0: no rotation)       */
+    int32_t pairs;        /* LQ_PAIRS_*                                          */
+    int32_t dtype;        /* q, k, outputs and gradients: LQ_DTYPE_*             */
+    float eps;            /* finite, > 0                                         */
+    float q_scale;        /* finite; multiplies q after the norm                 */
+} lq_qk_norm_config;
+
+typedef struct lq_qk_norm_args {
+    int64_t n_tokens;          /* >= 0                                            */
+    const void *q;             /* [n_tokens][heads_q][d], channels contiguous     */
+    const void *k;             /* [n_tokens][heads_k][d]                          */
+    const int32_t *positions;  /* int32 [n_tokens], any sign (rot_dim > 0)        */
+    const double *inv_freq;    /* f64 [rot_dim / 2], radians a position           */
+    const float *weight_q;     /* f32 [d]; NULL: 1                                */
+    const float *weight_k;     /* f32 [d]; NULL: 1                                */
+    int64_t q_token, q_head, k_token, k_head;   /* element strides of q and k     */
+} lq_qk_norm_args;
+
+/* One output, or one gradient, for each of q and k. */
+typedef struct lq_qk_pair {
+    void *q;
+    void *k;
+    int64_t q_token, q_head, k_token, k_head;   /* element strides                */
+} lq_qk_pair;
+
+/*
+ * Normalise and rotate.  `out` may be q and k themselves (same pointers and
+ * strides: in place).  Errors: LQ_ERR_INVALID_ARG for a bad config field, a
+ * NULL input or output that the config needs, a pointer not aligned to its
+ * element, or an output dimension of stride 0.
+ * Source: none (the pages take q and k as given).
+ */
+LQ_API lq_status lq_qk_norm_rotate(const lq_qk_norm_config *cfg, const lq_qk_norm_args *args,
+                                   const lq_qk_pair *out, void *stream);
+
+/* Device workspace of the backward pass (0 for an invalid config).
+ * Source: none (memory sizing). */
+LQ_API size_t lq_qk_norm_rotate_workspace_bytes(const lq_qk_norm_config *cfg);
+
+/*
+ * The gradients of lq_qk_norm_rotate(): `args` as in the forward call (q and k
+ * the original inputs), `grad_out` the gradients of its outputs (read only),
+ * `grad_in` those of q and k (may be grad_out itself: in place), grad_weight_q
+ * and grad_weight_k f32 [d] (NULL: not wanted; only where the weight is given).
+ * workspace: lq_qk_norm_rotate_workspace_bytes() bytes, 16-byte aligned; needed
+ * only with a weight gradient.  Errors: as lq_qk_norm_rotate(), and
+ * LQ_ERR_WORKSPACE for a missing or misaligned workspace.
+ * Source: none (the derivative of the norm and the rotation).
+ */
+LQ_API lq_status lq_qk_norm_rotate_backward(const lq_qk_norm_config *cfg, const lq_qk_norm_args *args,
+                                            const lq_qk_pair *grad_out, const lq_qk_pair *grad_in,
+                                            float *grad_weight_q, float *grad_weight_k, void *workspace,
+                                            void *stream);
+
 /* Text of the last error on the calling thread ("" if none).  Source: none. */
 LQ_API const char *lq_last_error_string(void);
 

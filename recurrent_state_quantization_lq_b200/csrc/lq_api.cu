@@ -5,30 +5,38 @@
 #include <cstdio>
 #include <cstring>
 #include <new>
-#include <string>
 #include <vector>
 
-#include "lq.h"
-#include <nvtx3/nvToolsExt.h>
-
+#include "lq_host.h"
 #include "lq_kernels.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace lq {
+
 lq_status fail(lq_status code, const std::string &why) {
     g_last_error = why;
     return code;
 }
+
+}  // namespace lq
+
+namespace {
+
+using lq::aligned;
+using lq::cuda_fail;
+using lq::fail;
+using lq::Range;
 
 constexpr uint32_t kMagic = 0x4c515354u;  // "LQST"
 constexpr int kMaxComp = 8;
 constexpr int kMaxWindow = 4096;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool validate(const lq_config *c, std::string *why) {
     if (c == nullptr) { *why = "config is NULL"; return false; }
@@ -101,10 +109,6 @@ T *region(unsigned char *base, size_t off) {
     return off == LQ_ABSENT ? nullptr : reinterpret_cast<T *>(base + off);
 }
 
-lq_status cuda_fail(cudaError_t e, const char *what) {
-    return fail(LQ_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
 }  // namespace
 
 struct lq_state_s {
@@ -127,15 +131,6 @@ struct lq_state_s {
 namespace {
 
 bool check_handle(lq_handle h) { return h != nullptr && h->magic == kMagic; }
-
-// An NVTX range around a stream-ordered call, for timeline tools (nsys, ncu);
-// nearly free when no tool is attached.
-struct Range {
-    explicit Range(const char *name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range &) = delete;
-    Range &operator=(const Range &) = delete;
-};
 
 lq::Views views(lq_handle h) {
     lq::Views v;

@@ -1,0 +1,31 @@
+// Host-side launchers of the stateless operators (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "lq.h"
+
+namespace lq {
+
+// Tokens between two checkpoints of the gated scan: what one CTA of the
+// backward pass takes at a time.
+int scan_checkpoint_tokens(int d);
+
+// `vec`: every pointer and stride of the call lets a thread move eight
+// channels with 16-byte accesses, and d is a multiple of 8.
+cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, bool vec, cudaStream_t s);
+cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a, const lq_scan_grads &g, bool vec,
+                                 cudaStream_t s);
+
+// Partial weight gradients that the norm's backward pass writes at most: one
+// for each CTA and each of q and k.
+constexpr int kQkPartials = 1024;
+
+cudaError_t launch_qk_norm(const lq_qk_norm_config &c, const lq_qk_norm_args &a, const lq_qk_pair &out,
+                           cudaStream_t s);
+cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm_args &a, const lq_qk_pair &grad_out,
+                                    const lq_qk_pair &grad_in, float *grad_wq, float *grad_wk, float *partials,
+                                    cudaStream_t s);
+
+}  // namespace lq

@@ -26,6 +26,8 @@ GATE = {"scalar": 0, "gdn": 0, "channel": 1, "kda": 1}
 MODE = {"window": 0, "naive": 1, "fp32": 2}
 SELECT = {"l2": 0, "maxabs": 1}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+NORM = {"l2": 0, "rms": 1}
+PAIRS = {"half": 0, "neighbours": 1}
 ABSENT = ctypes.c_size_t(-1).value
 
 LQ_DEVERR_BOUNDS = 4   # device error code: an index out of range (checked build; unit tickets in every build)
@@ -55,6 +57,42 @@ EXPORT_REGIONS = ("codes", "row_scale", "col_smooth", "comp_index", "comp_row_ve
 class Export(ctypes.Structure):
     """lq_export: destination pointers of lq_state_export (NULL = not copied)."""
     _fields_ = [(n, ctypes.c_void_p) for n in EXPORT_REGIONS]
+
+
+class Strides(ctypes.Structure):
+    """lq_strides, in elements."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("token", "seq", "head")]
+
+
+class ScanConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads", "d", "gate", "in_dtype", "out_dtype")]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)] + \
+        [(n, ctypes.c_void_p) for n in ("v", "g", "beta", "h0", "lengths", "out", "h_last", "checkpoints")] + \
+        [(n, Strides) for n in ("v_stride", "g_stride", "beta_stride", "out_stride")]
+
+
+class ScanGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("grad_out", "grad_last", "grad_v", "grad_g", "grad_beta", "grad_h0")] + \
+        [(n, Strides) for n in ("grad_out_stride", "grad_v_stride", "grad_g_stride", "grad_beta_stride")]
+
+
+class QkNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads_q", "heads_k", "d", "norm", "rot_dim", "pairs", "dtype")] + \
+        [(n, ctypes.c_float) for n in ("eps", "q_scale")]
+
+
+class QkNormArgs(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("q", "k", "positions", "inv_freq", "weight_q", "weight_k")] + \
+        [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head")]
+
+
+class QkPair(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head")]
 
 
 class LQError(RuntimeError):
@@ -107,6 +145,18 @@ def lib() -> ctypes.CDLL:
         L.lq_device_status.restype = i32
         L.lq_state_destroy.argtypes = [vp]
         L.lq_state_destroy.restype = i32
+        L.lq_gated_scan_checkpoint_bytes.argtypes = [vp, i32]
+        L.lq_gated_scan_checkpoint_bytes.restype = ctypes.c_size_t
+        L.lq_gated_scan.argtypes = [vp, vp, vp]
+        L.lq_gated_scan.restype = i32
+        L.lq_gated_scan_backward.argtypes = [vp, vp, vp, vp]
+        L.lq_gated_scan_backward.restype = i32
+        L.lq_qk_norm_rotate.argtypes = [vp, vp, vp, vp]
+        L.lq_qk_norm_rotate.restype = i32
+        L.lq_qk_norm_rotate_workspace_bytes.argtypes = [vp]
+        L.lq_qk_norm_rotate_workspace_bytes.restype = ctypes.c_size_t
+        L.lq_qk_norm_rotate_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+        L.lq_qk_norm_rotate_backward.restype = i32
         L.lq_last_error_string.argtypes = []
         L.lq_last_error_string.restype = ctypes.c_char_p
         _lib = L
@@ -150,6 +200,240 @@ def _stream_ptr(stream, device) -> ctypes.c_void_p:
 
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
     return ctypes.c_void_p(None if t is None else t.data_ptr())
+
+
+# ------------------------------------------------------- stateless operators
+def _on(x: torch.Tensor, stream):
+    """None when `x`'s device and the given stream are the current ones; else
+    the context that makes them so, for the launch and what it allocates."""
+    assert x.is_cuda, "a CUDA tensor is needed"
+    if stream is None:
+        return None if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+    assert stream.device == x.device, (stream.device, x.device)
+    return torch.cuda.stream(stream)
+
+
+def _tensor(x: torch.Tensor | None, what: str, like: torch.Tensor, dtype, shape, packed: bool = True):
+    """Check one tensor argument (None is a NULL pointer) and return its address."""
+    if x is None:
+        return None
+    assert x.device == like.device, (what, x.device, like.device)
+    assert x.dtype == dtype, (what, x.dtype, dtype)
+    assert x.shape == shape, (what, tuple(x.shape), tuple(shape))
+    assert not packed or x.is_contiguous(), f"{what} must be contiguous"
+    return x.data_ptr()
+
+
+def _rows(x: torch.Tensor | None, what: str, like: torch.Tensor, dtype, shape):
+    """Check a [T, batch, heads(, d)] tensor of any strides whose channels are
+    contiguous; its address and its Strides."""
+    if x is None:
+        return None, (0, 0, 0)
+    p = _tensor(x, what, like, dtype, shape, packed=False)
+    s = x.stride()
+    assert len(s) == 3 or s[3] == 1 or shape[3] == 1, f"{what}: channels must be contiguous"
+    return p, s[:3]
+
+
+def _scan_config(v: torch.Tensor, g: torch.Tensor, out_dtype) -> ScanConfig:
+    assert v.dim() == 4, "v is [T, batch, heads, d]"
+    assert g.shape == v.shape or g.shape == v.shape[:3], "g is [T, batch, heads] or [T, batch, heads, d]"
+    T, B, H, d = v.shape
+    return ScanConfig(B, H, d, int(g.dim() == 4), DTYPE[v.dtype], DTYPE[out_dtype])
+
+
+def gated_scan_checkpoints(v: torch.Tensor, g: torch.Tensor) -> torch.Tensor:
+    """The buffer that gated_scan(checkpoints=) fills for gated_scan_backward()
+    on inputs of these shapes."""
+    cfg = _scan_config(v, g, v.dtype)
+    n = lib().lq_gated_scan_checkpoint_bytes(ctypes.byref(cfg), v.shape[0])
+    if n == 0 and v.shape[0] > 0:
+        raise LQError(LQ_ERR_INVALID_ARG, "lq_gated_scan_checkpoint_bytes")
+    return torch.empty(n // 4, dtype=torch.float32, device=v.device)
+
+
+def _scan_args(v, g, beta, lengths, checkpoints, out_dtype):
+    cfg = _scan_config(v, g, out_dtype)
+    T, B, H, d = v.shape
+    pv, sv = _rows(v, "v", v, v.dtype, v.shape)
+    pg, sg = _rows(g, "g", v, torch.float32, g.shape)
+    pb, sb = _rows(beta, "beta", v, torch.float32, v.shape[:3])
+    pl = _tensor(lengths, "lengths", v, torch.int32, (B,))
+    if checkpoints is not None:
+        n = lib().lq_gated_scan_checkpoint_bytes(ctypes.byref(cfg), T) // 4
+        assert checkpoints.numel() >= n, "checkpoints of another shape: see gated_scan_checkpoints()"
+    pc = _tensor(checkpoints, "checkpoints", v, torch.float32, () if checkpoints is None else checkpoints.shape)
+    return cfg, ScanArgs(T, 0, pv, pg, pb, None, pl, None, None, pc, sv, sg, sb, (0, 0, 0))
+
+
+def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None, checkpoints=None, out_dtype=None,
+               want_out: bool = True, stream=None):
+    """The gated linear recurrence h_t = exp(g_t) h_{t-1} + beta_t v_t over
+    vector states (lq_gated_scan): v [T, batch, heads, d] (BF16 or FP32, any
+    strides with contiguous channels; transpose a [batch, T, ...] tensor), g
+    FP32 [T, batch, heads] or [T, batch, heads, d], beta FP32 [T, batch, heads]
+    (None: 1), h0 FP32 [batch, heads, d] (None: zero), lengths int32 [batch]
+    on the device (None: T).  Returns (out, h_last): every h_t in out_dtype
+    (default v's), zero past a sequence's length, and the FP32 state after its
+    last token.  `out` and `h_last` may be given (rows of `out` past a length
+    then stay as they are; h_last may be h0); want_out=False skips `out`.
+    `checkpoints` (gated_scan_checkpoints()) is filled for the backward pass."""
+    on = _on(v, stream)
+    if on is not None:
+        with on:
+            return gated_scan(v, g, beta, h0, lengths=lengths, out=out, h_last=h_last, checkpoints=checkpoints,
+                              out_dtype=out_dtype, want_out=want_out)
+    out_dtype = out.dtype if out is not None else out_dtype or v.dtype
+    cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
+    if out is None and want_out:
+        out = (torch.empty_like if lengths is None else torch.zeros_like)(v, dtype=out_dtype)
+    if h_last is None:
+        h_last = torch.empty(v.shape[1:], dtype=torch.float32, device=v.device)
+    args.h0 = _tensor(h0, "h0", v, torch.float32, v.shape[1:])
+    args.h_last = _tensor(h_last, "h_last", v, torch.float32, v.shape[1:])
+    args.out, args.out_stride = _rows(out, "out", v, out_dtype, v.shape)
+    st = lib().lq_gated_scan(ctypes.byref(cfg), ctypes.byref(args), _stream_ptr(None, v.device))
+    if st != LQ_OK:
+        raise LQError(st, "lq_gated_scan")
+    return out, h_last
+
+
+def gated_scan_backward(grad_out, v, g, beta=None, *, checkpoints, grad_last=None, lengths=None, grad_v=None,
+                        grad_g=None, grad_beta=None, grad_h0=None, stream=None):
+    """The gradients of gated_scan() (lq_gated_scan_backward): v, g, beta and
+    lengths as in the forward call, `checkpoints` as it filled them, grad_out
+    like out (None: zero), grad_last FP32 like h_last (None: zero).  Returns
+    (grad_v, grad_g, grad_beta, grad_h0); grad_beta is None without beta.
+    Tokens past a length get zero, or stay as they are in a tensor given for
+    the result."""
+    on = _on(v, stream)
+    if on is not None:
+        with on:
+            return gated_scan_backward(grad_out, v, g, beta, checkpoints=checkpoints, grad_last=grad_last,
+                                       lengths=lengths, grad_v=grad_v, grad_g=grad_g, grad_beta=grad_beta,
+                                       grad_h0=grad_h0)
+    out_dtype = v.dtype if grad_out is None else grad_out.dtype
+    cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
+    new = torch.empty_like if lengths is None else torch.zeros_like
+    grad_v = new(v) if grad_v is None else grad_v
+    grad_g = new(g) if grad_g is None else grad_g
+    if beta is not None and grad_beta is None:
+        grad_beta = new(beta)
+    if grad_h0 is None:
+        grad_h0 = torch.empty(v.shape[1:], dtype=torch.float32, device=v.device)
+    grads = ScanGrads()
+    grads.grad_out, grads.grad_out_stride = _rows(grad_out, "grad_out", v, out_dtype, v.shape)
+    grads.grad_v, grads.grad_v_stride = _rows(grad_v, "grad_v", v, v.dtype, v.shape)
+    grads.grad_g, grads.grad_g_stride = _rows(grad_g, "grad_g", v, torch.float32, g.shape)
+    grads.grad_beta, grads.grad_beta_stride = _rows(grad_beta, "grad_beta", v, torch.float32, v.shape[:3])
+    grads.grad_last = _tensor(grad_last, "grad_last", v, torch.float32, v.shape[1:])
+    grads.grad_h0 = _tensor(grad_h0, "grad_h0", v, torch.float32, v.shape[1:])
+    st = lib().lq_gated_scan_backward(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(grads),
+                                      _stream_ptr(None, v.device))
+    if st != LQ_OK:
+        raise LQError(st, "lq_gated_scan_backward")
+    return grad_v, grad_g, grad_beta, grad_h0
+
+
+def _heads_of(x: torch.Tensor, what: str, like: torch.Tensor, lead) -> tuple:
+    """Check a [..., heads, d] tensor; its address, token stride and head stride."""
+    assert x.device == like.device and x.dtype == like.dtype, (what, x.device, x.dtype)
+    assert x.dim() >= 2 and x.shape[:-2] == lead and x.shape[-1] == like.shape[-1], (what, tuple(x.shape))
+    s = x.stride()
+    assert s[-1] == 1 or x.shape[-1] == 1, f"{what}: channels must be contiguous"
+    token, n = 0, 1
+    for size, step in zip(reversed(lead), reversed(s[:-2])):      # the tokens lie at one stride
+        if size == 1:
+            continue
+        if n == 1:
+            token = step
+        assert n == 1 or step == token * n, f"{what}: its leading dimensions are not one run of tokens"
+        n *= size
+    return x.data_ptr(), token, s[-2] if x.shape[-2] > 1 else x.shape[-1]
+
+
+def _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale):
+    lead, d = q.shape[:-2], q.shape[-1]
+    n = q.shape[:-2].numel()
+    heads_k = 0 if k is None else k.shape[-2]
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    cfg = QkNormConfig(q.shape[-2], heads_k, d, NORM[norm], rot, PAIRS[pairs], DTYPE[q.dtype], eps, q_scale)
+    pq, tq, hq = _heads_of(q, "q", q, lead)
+    pk, tk, hk = (None, 0, 0) if k is None else _heads_of(k, "k", q, lead)
+    if rot:
+        assert positions is not None, "a rotation needs positions"
+    return cfg, QkNormArgs(n, pq, pk, _tensor(positions, "positions", q, torch.int32, lead) if rot else None,
+                           _tensor(inv_freq, "inv_freq", q, torch.float64, (rot // 2,)),
+                           _tensor(weight_q, "weight_q", q, torch.float32, (d,)),
+                           _tensor(weight_k, "weight_k", q, torch.float32, (d,)), tq, hq, tk, hk)
+
+
+def _qk_pair(q, k, like_q, like_k, what) -> QkPair:
+    assert q.shape == like_q.shape and (k is None) == (like_k is None) and (k is None or k.shape == like_k.shape), what
+    lead = like_q.shape[:-2]
+    pq, tq, hq = _heads_of(q, what, like_q, lead)
+    pk, tk, hk = (None, 0, 0) if k is None else _heads_of(k, what, like_q, lead)
+    return QkPair(pq, pk, tq, hq, tk, hk)
+
+
+def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, weight_k=None, norm: str = "l2",
+                   eps: float = 1e-6, pairs: str = "half", q_scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Normalise every head of q [..., heads_q, d] and k [..., heads_k, d]
+    (BF16 or FP32; views into a fused projection will do), then rotate its
+    first 2 * len(inv_freq) channels by positions * inv_freq and multiply q by
+    q_scale (lq_qk_norm_rotate).  norm: "l2" or "rms"; weights FP32 [d] (None:
+    1); positions int32 [...]; inv_freq FP64 [rot_dim / 2] (None: no
+    rotation); pairs: "half" (i with i + rot_dim / 2) or "neighbours" (2 i
+    with 2 i + 1).  Returns (q_out, k_out), new tensors unless given; they may
+    be q and k themselves."""
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return qk_norm_rotate(q, k, positions=positions, inv_freq=inv_freq, weight_q=weight_q, weight_k=weight_k,
+                                  norm=norm, eps=eps, pairs=pairs, q_scale=q_scale, q_out=q_out, k_out=k_out)
+    cfg, args = _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    out = _qk_pair(q_out, k_out, q, k, "an output")
+    st = lib().lq_qk_norm_rotate(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(out), _stream_ptr(None, q.device))
+    if st != LQ_OK:
+        raise LQError(st, "lq_qk_norm_rotate")
+    return q_out, k_out
+
+
+def qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k=None, *, positions=None, inv_freq=None, weight_q=None,
+                            weight_k=None, norm: str = "l2", eps: float = 1e-6, pairs: str = "half",
+                            q_scale: float = 1.0, grad_q=None, grad_k=None, stream=None):
+    """The gradients of qk_norm_rotate() (lq_qk_norm_rotate_backward): q, k and
+    the keywords as in the forward call, grad_q_out and grad_k_out those of
+    its results.  Returns (grad_q, grad_k, grad_weight_q, grad_weight_k), the
+    last two FP32 [d], None where there is no weight."""
+    on = _on(q, stream)
+    if on is not None:
+        with on:
+            return qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k, positions=positions, inv_freq=inv_freq,
+                                           weight_q=weight_q, weight_k=weight_k, norm=norm, eps=eps, pairs=pairs,
+                                           q_scale=q_scale, grad_q=grad_q, grad_k=grad_k)
+    cfg, args = _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
+    gy = _qk_pair(grad_q_out, grad_k_out, q, k, "a gradient of an output")
+    grad_q = torch.empty(q.shape, dtype=q.dtype, device=q.device) if grad_q is None else grad_q
+    if k is not None and grad_k is None:
+        grad_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    gx = _qk_pair(grad_q, grad_k, q, k, "a gradient of an input")
+    gwq = None if weight_q is None else torch.empty_like(weight_q)
+    gwk = None if weight_k is None else torch.empty_like(weight_k)
+    work = None
+    if gwq is not None or gwk is not None:
+        n = lib().lq_qk_norm_rotate_workspace_bytes(ctypes.byref(cfg))
+        if n == 0:
+            raise LQError(LQ_ERR_INVALID_ARG, "lq_qk_norm_rotate_workspace_bytes")
+        work = torch.empty(n, dtype=torch.uint8, device=q.device)
+    st = lib().lq_qk_norm_rotate_backward(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(gy), ctypes.byref(gx),
+                                          _ptr(gwq), _ptr(gwk), _ptr(work), _stream_ptr(None, q.device))
+    if st != LQ_OK:
+        raise LQError(st, "lq_qk_norm_rotate_backward")
+    return grad_q, grad_k, gwq, gwk
 
 
 class DecodeState:

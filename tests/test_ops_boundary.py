@@ -1,0 +1,150 @@
+"""Refusals of the stateless operators, without a GPU: every call below returns before any launch."""
+import ctypes
+
+import pytest
+import torch
+
+from recurrent_state_quantization_lq_b200 import lq
+
+P = 1 << 21                         # addresses that nothing reads
+ref = ctypes.byref
+
+
+def scan_config(**kw):
+    return lq.ScanConfig(**{"batch": 2, "heads": 3, "d": 64, "gate": 0, "in_dtype": 1, "out_dtype": 1, **kw})
+
+
+def scan_args(**kw):
+    a = lq.ScanArgs(n_tokens=4, v=P, g=P, beta=P, h0=P, out=P, h_last=P, checkpoints=P, v_stride=(384, 192, 64),
+                    g_stride=(6, 3, 1), beta_stride=(6, 3, 1), out_stride=(384, 192, 64))
+    for n, x in kw.items():
+        setattr(a, n, x)
+    return a
+
+
+def scan_grads(**kw):
+    g = lq.ScanGrads(grad_out=P, grad_last=P, grad_v=P, grad_g=P, grad_beta=P, grad_h0=P,
+                     grad_out_stride=(384, 192, 64), grad_v_stride=(384, 192, 64), grad_g_stride=(6, 3, 1),
+                     grad_beta_stride=(6, 3, 1))
+    for n, x in kw.items():
+        setattr(g, n, x)
+    return g
+
+
+@pytest.mark.parametrize("field,value", [("batch", 0), ("heads", 0), ("heads", 1 << 24), ("d", 0), ("d", 257), ("gate", 2),
+                                         ("in_dtype", 2), ("out_dtype", -1)])
+def test_scan_configs_refused(field, value):
+    L, cfg = lq.lib(), scan_config(**{field: value})
+    assert L.lq_gated_scan_checkpoint_bytes(ref(cfg), 4) == 0 and lq.last_error()
+    assert L.lq_gated_scan(ref(cfg), ref(scan_args()), None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args()), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw,word", [({"n_tokens": -1}, "negative"), ({"reserved": 1}, "reserved"), ({"v": None}, "NULL"),
+                                     ({"g": None}, "NULL"), ({"v": P + 1}, "aligned"), ({"g": P + 2}, "aligned"),
+                                     ({"lengths": P + 1}, "aligned"), ({"h0": P + 2}, "aligned"),
+                                     ({"checkpoints": P + 3}, "aligned"), ({"beta": P + 1}, "aligned")])
+def test_scan_arguments_refused(kw, word):
+    L, cfg = lq.lib(), scan_config()
+    assert L.lq_gated_scan(ref(cfg), ref(scan_args(**kw)), None) == lq.LQ_ERR_INVALID_ARG
+    assert word in lq.last_error()
+    assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args(**kw)), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
+    assert word in lq.last_error()
+
+
+def test_scan_outputs_and_gradients_refused():
+    L, cfg = lq.lib(), scan_config()
+    for kw in ({"out": P + 1}, {"h_last": P + 2}, {"out_stride": (0, 192, 64)}, {"out_stride": (384, 0, 64)},
+               {"out_stride": (384, 192, 0)}):
+        assert L.lq_gated_scan(ref(cfg), ref(scan_args(**kw)), None) == lq.LQ_ERR_INVALID_ARG, kw
+    assert L.lq_gated_scan(ref(cfg), None, None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_gated_scan(None, ref(scan_args()), None) == lq.LQ_ERR_INVALID_ARG
+    for kw in ({"grad_v": P + 1}, {"grad_g": P + 2}, {"grad_beta": P + 2}, {"grad_out": P + 1}, {"grad_last": P + 2},
+               {"grad_h0": P + 2}, {"grad_v_stride": (0, 192, 64)}, {"grad_g_stride": (6, 3, 0)},
+               {"grad_beta_stride": (6, 0, 1)}):
+        assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args()), ref(scan_grads(**kw)), None) == lq.LQ_ERR_INVALID_ARG, kw
+    assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args()), None, None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args(checkpoints=None)), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
+    assert "checkpoints" in lq.last_error()
+    assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args(beta=None)), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
+    assert "grad_beta" in lq.last_error()
+
+
+@pytest.mark.parametrize("d", [1, 8, 9, 64, 65, 128, 129, 256])
+def test_checkpoints_are_small_and_grow_with_the_tokens(d):
+    L, cfg = lq.lib(), scan_config(d=d)
+    size = [L.lq_gated_scan_checkpoint_bytes(ref(cfg), n) for n in (0, 1, 32, 33, 4096, 1 << 20)]
+    assert size[0] == 0 and size[1] == 6 * d * 4 and size == sorted(size)
+    assert size[-1] <= (1 << 20) // 32 * 6 * d * 4
+    assert L.lq_gated_scan_checkpoint_bytes(ref(cfg), -1) == 0
+
+
+def qk_config(**kw):
+    return lq.QkNormConfig(**{"heads_q": 4, "heads_k": 2, "d": 64, "norm": 0, "rot_dim": 64, "pairs": 0, "dtype": 1,
+                              "eps": 1e-6, "q_scale": 1.0, **kw})
+
+
+def qk_args(**kw):
+    return lq.QkNormArgs(**{"n_tokens": 5, "q": P, "k": P, "positions": P, "inv_freq": P, "weight_q": P, "weight_k": P,
+                            "q_token": 256, "q_head": 64, "k_token": 128, "k_head": 64, **kw})
+
+
+def pair(**kw):
+    return lq.QkPair(**{"q": P, "k": P, "q_token": 256, "q_head": 64, "k_token": 128, "k_head": 64, **kw})
+
+
+@pytest.mark.parametrize("kw", [{"heads_q": 0}, {"heads_k": -1}, {"d": 0}, {"d": 257}, {"norm": 2}, {"rot_dim": 63},
+                                {"rot_dim": 66}, {"rot_dim": -2}, {"pairs": 2}, {"dtype": 3}, {"eps": 0.0}, {"eps": -1.0},
+                                {"eps": float("nan")}, {"eps": float("inf")}, {"q_scale": float("inf")}])
+def test_qk_configs_refused(kw):
+    L, cfg = lq.lib(), qk_config(**kw)
+    assert L.lq_qk_norm_rotate_workspace_bytes(ref(cfg)) == 0 and lq.last_error()
+    assert L.lq_qk_norm_rotate(ref(cfg), ref(qk_args()), ref(pair()), None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_qk_norm_rotate_backward(ref(cfg), ref(qk_args()), ref(pair()), ref(pair()), P, P, P,
+                                        None) == lq.LQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [{"n_tokens": -1}, {"n_tokens": 1 << 31}, {"q": None}, {"k": None}, {"positions": None},
+                                {"inv_freq": None}, {"q": P + 1}, {"inv_freq": P + 4}, {"positions": P + 2},
+                                {"weight_q": P + 2}])
+def test_qk_arguments_refused(kw):
+    L, cfg = lq.lib(), qk_config()
+    assert L.lq_qk_norm_rotate(ref(cfg), ref(qk_args(**kw)), ref(pair()), None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_qk_norm_rotate_backward(ref(cfg), ref(qk_args(**kw)), ref(pair()), ref(pair()), None, None, None,
+                                        None) == lq.LQ_ERR_INVALID_ARG
+
+
+def test_qk_outputs_and_workspaces_refused():
+    L, cfg = lq.lib(), qk_config()
+    for kw in ({"q": None}, {"k": None}, {"q": P + 1}, {"q_token": 0}, {"k_head": 0}):
+        assert L.lq_qk_norm_rotate(ref(cfg), ref(qk_args()), ref(pair(**kw)), None) == lq.LQ_ERR_INVALID_ARG, kw
+        assert L.lq_qk_norm_rotate_backward(ref(cfg), ref(qk_args()), ref(pair()), ref(pair(**kw)), None, None, None,
+                                            None) == lq.LQ_ERR_INVALID_ARG, kw
+    back = L.lq_qk_norm_rotate_backward
+    assert back(ref(cfg), ref(qk_args()), ref(pair()), ref(pair()), P, P, None, None) == lq.LQ_ERR_WORKSPACE
+    assert back(ref(cfg), ref(qk_args()), ref(pair()), ref(pair()), P, P, P + 4, None) == lq.LQ_ERR_WORKSPACE
+    assert back(ref(cfg), ref(qk_args(weight_q=None)), ref(pair()), ref(pair()), P, None, P, None) == lq.LQ_ERR_INVALID_ARG
+    assert back(ref(cfg), ref(qk_args()), None, ref(pair()), None, None, None, None) == lq.LQ_ERR_INVALID_ARG
+    assert L.lq_qk_norm_rotate(ref(cfg), ref(qk_args()), None, None) == lq.LQ_ERR_INVALID_ARG
+
+
+def test_the_binding_refuses_host_tensors():
+    v, g = torch.zeros(4, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 2)
+    for call in (lambda: lq.gated_scan(v, g), lambda: lq.qk_norm_rotate(v, v),
+                 lambda: lq.gated_scan_backward(v, v, g, checkpoints=None)):
+        with pytest.raises(AssertionError, match="CUDA"):
+            call()
+
+
+def test_structs_match_the_header():
+    """Field names and order of the binding's structs are the header's."""
+    import re
+    with open(lq.HEADER) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    for name, struct in (("lq_strides", lq.Strides), ("lq_scan_config", lq.ScanConfig), ("lq_scan_args", lq.ScanArgs),
+                         ("lq_scan_grads", lq.ScanGrads), ("lq_qk_norm_config", lq.QkNormConfig),
+                         ("lq_qk_norm_args", lq.QkNormArgs), ("lq_qk_pair", lq.QkPair)):
+        body = re.search(r"typedef struct %s \{(.*?)\} %s;" % (name, name), text, re.S).group(1)
+        fields = [f.strip(" *") for line in body.split(";") if line.strip()
+                  for f in re.sub(r"^\s*(const )?\w+\s", "", line.strip()).split(",")]
+        assert fields == [n for n, _ in struct._fields_], name
