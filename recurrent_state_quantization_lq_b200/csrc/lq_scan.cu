@@ -10,9 +10,13 @@
 //
 // A thread holds eight channels of a row (lq_vec8.cuh); row_lanes(d) adjacent
 // lanes hold a row.
+#include <cooperative_groups.h>
+
 #include "lq_ops.h"
 #include "lq_kernels.h"
 #include "lq_vec8.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace lq {
 
@@ -75,6 +79,10 @@ struct Gates {
 #pragma unroll
         for (int i = 0; i < (CHAN ? 8 : 1); ++i) a[i] = gate_of(a[i]);
     }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (CHAN ? 8 : 1); ++i) a[i] = 0.0f;
+    }
     __device__ __forceinline__ void one() {
 #pragma unroll
         for (int i = 0; i < (CHAN ? 8 : 1); ++i) a[i] = 1.0f;
@@ -115,6 +123,146 @@ __global__ void __launch_bounds__(kScanThreads) scan_rows_kernel(lq_scan_args a,
         if (a.out != nullptr) store8<VEC>(static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t) + c0, n, h);
     }
     if (a.h_last != nullptr) store8<VEC>(a.h_last + state, n, h);
+}
+
+// A cluster of CTAs takes one unit: `ranks` CTAs x (rows of lanes) x R
+// consecutive tokens at a time.  Each row runs its tokens from zero, the rows'
+// maps are composed over the warp by shuffles, over the CTA's warps by one
+// thread a channel and over the cluster through distributed shared memory;
+// every CTA composes all of the cluster's maps, so each knows the state that
+// the next tokens start from.  The row then runs its tokens, still in
+// registers, again from their true start and stores them: every input is read
+// and every output written once.
+template <typename InT, bool CHAN>
+struct ForwardRun {
+    // 64 bytes of v a row at least in flight per thread, and no more registers than three CTAs an SM leave
+    static constexpr int R = sizeof(InT) == 2 && !CHAN ? 8 : 4;
+};
+
+template <typename InT, typename OutT, bool CHAN, bool VEC>
+__global__ void __launch_bounds__(kScanThreads)
+    scan_split_kernel(lq_scan_args a, int heads, int units, int d, int lanes, int every) {
+    constexpr int NW = kScanThreads / 32, R = ForwardRun<InT, CHAN>::R, MAXD = 256;
+    __shared__ float sA[NW][CHAN ? MAXD : 1], sH[NW][MAXD];   // the warps' maps, then the states before their tokens
+    __shared__ float2 mine[2][MAXD];                          // this CTA's map (A, H), by the parity of the step
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int rows = kScanThreads / lanes, chunk = rows * R;
+    const int c0 = (lane % lanes) * 8, row = tid / lanes;
+    const Unit w = unit_of(a, heads, blockIdx.x / ranks);
+    const bool on = c0 < d;
+    const int n = on ? min(8, d - c0) : 0;
+    float carry = 0.0f;              // thread c < d: the state before the step's tokens
+    if (tid < d && a.h0 != nullptr) carry = a.h0[(int64_t)w.u * d + tid];
+
+    int step = 0;
+    for (int t0 = 0; t0 < w.len; t0 += ranks * chunk, ++step) {
+        const int t_row = t0 + rank * chunk + row * R;
+        Raw8<InT> rv[R];
+        Gates<CHAN, VEC> gate[R];
+        float beta[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            zero8(rv[i]);
+            gate[i].zero();
+            beta[i] = 1.0f;
+            const int t = t_row + i;
+            if (t < w.len && on) {
+                load8<VEC>(static_cast<const InT *>(a.v) + row_of(a.v_stride, w, t) + c0, n, rv[i]);
+                gate[i].load(a.g + row_of(a.g_stride, w, t) + (CHAN ? c0 : 0), n);
+                if (a.beta != nullptr) beta[i] = __ldg(a.beta + row_of(a.beta_stride, w, t));
+            }
+        }
+        Gates<CHAN, VEC> A;
+        float H[8] = {};
+        A.one();
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float v[8];
+            gate[i].exponentiate();
+            widen8(rv[i], v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) H[c] = fmaf(gate[i][c], H[c], beta[i] * v[c]);
+#pragma unroll
+            for (int c = 0; c < (CHAN ? 8 : 1); ++c) A.a[c] *= gate[i].a[c];
+        }
+        for (int o = lanes; o < 32; o *= 2) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float hp = __shfl_up_sync(0xffffffffu, H[c], o);
+                if (lane >= o) H[c] = fmaf(A[c], hp, H[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < (CHAN ? 8 : 1); ++c) {
+                const float ap = __shfl_up_sync(0xffffffffu, A.a[c], o);
+                if (lane >= o) A.a[c] *= ap;
+            }
+        }
+        if (on && lane >= 32 - lanes) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c0 + c < d) {
+                    sH[warp][c0 + c] = H[c];
+                    if (CHAN) sA[warp][c0 + c] = A[c];
+                }
+            if (!CHAN) sA[warp][0] = A.a[0];
+        }
+        __syncthreads();
+        float pa[NW], ph[NW], ca = 1.0f, ch = 0.0f;
+        if (tid < d) {
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {           // the map of the warps before warp k
+                pa[k] = ca;
+                ph[k] = ch;
+                const float ak = sA[k][CHAN ? tid : 0];
+                ch = fmaf(ak, ch, sH[k][tid]);
+                ca *= ak;
+            }
+        }
+        float before = carry;
+        if (ranks > 1) {
+            if (tid < d) mine[step & 1][tid] = make_float2(ca, ch);
+            // one barrier a step: the other parity's maps are written next, and
+            // these only after every CTA has passed the next barrier
+            cluster.sync();
+            if (tid < d) {
+                for (int r = 0; r < ranks; ++r) {
+                    if (r == rank) before = carry;
+                    const float2 m = cluster.map_shared_rank(&mine[step & 1][0], r)[tid];
+                    carry = fmaf(m.x, carry, m.y);
+                }
+            }
+        } else {
+            carry = fmaf(ca, carry, ch);
+        }
+        if (tid < d) {
+#pragma unroll
+            for (int k = 0; k < NW; ++k) sH[k][tid] = fmaf(pa[k], before, ph[k]);
+        }
+        __syncthreads();
+        float h[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {                // the map of the warp's rows before this one, then the warp's start
+            const float hp = __shfl_up_sync(0xffffffffu, H[c], lanes), ap = __shfl_up_sync(0xffffffffu, A[c], lanes);
+            const float hs = c0 + c < d ? sH[warp][c0 + c] : 0.0f;
+            h[c] = lane >= lanes ? fmaf(ap, hs, hp) : hs;
+        }
+        if (a.checkpoints != nullptr && on && t_row % every == 0 && t_row < w.len)
+            store8<VEC>(a.checkpoints + ((int64_t)(t_row / every) * units + w.u) * d + c0, n, h);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float v[8];
+            widen8(rv[i], v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) h[c] = fmaf(gate[i][c], h[c], beta[i] * v[c]);
+            if (a.out != nullptr && on && t_row + i < w.len)
+                store8<VEC>(static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t_row + i) + c0, n, h);
+        }
+        __syncthreads();                             // sH is read: the next step may write it
+    }
+    if (tid < d && rank == 0 && a.h_last != nullptr) a.h_last[(int64_t)w.u * d + tid] = carry;
+    if (ranks > 1) cluster.sync();                   // no CTA leaves while another reads its map
 }
 
 // ------------------------------------------------------------------ backward
@@ -307,15 +455,44 @@ cudaError_t by_variant(const lq_scan_config &c, bool vec, F &&f) {
 
 }  // namespace
 
+// A launch of `ranks` CTAs a unit as clusters.
+template <typename... P, typename... V>
+cudaError_t launch_clusters(void (*kernel)(P...), int units, int ranks, cudaStream_t s, const V &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)units * (unsigned)ranks);
+    cfg.blockDim = dim3(kScanThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs that share a unit: as many as fill the device about twice over, up to
+// the portable cluster size and to what the tokens keep busy.
+int ranks_of(int units, long long tokens, int chunk) {
+    int ranks = 1;
+    while (ranks < 8 && (long long)units * ranks < 2 * sm_count() && (long long)ranks * chunk < tokens) ranks *= 2;
+    return ranks;
+}
+
 cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, bool vec, cudaStream_t s) {
-    const int units = c.batch * c.heads, lanes = row_lanes(c.d);
+    const int units = c.batch * c.heads, lanes = row_lanes(c.d), every = scan_checkpoint_tokens(c.d);
     return by_variant(c, vec, [&](auto k) {
         using K = decltype(k);
-        const long long threads = (long long)units * lanes;
-        scan_rows_kernel<typename K::In, typename K::Out, K::CHAN, K::VEC>
-            <<<(unsigned)((threads + kScanThreads - 1) / kScanThreads), kScanThreads, 0, s>>>(
-                a, c.heads, units, c.d, lanes, scan_checkpoint_tokens(c.d));
-        return cudaGetLastError();
+        if (a.n_tokens <= 4) {
+            const long long threads = (long long)units * lanes;
+            scan_rows_kernel<typename K::In, typename K::Out, K::CHAN, K::VEC>
+                <<<(unsigned)((threads + kScanThreads - 1) / kScanThreads), kScanThreads, 0, s>>>(
+                    a, c.heads, units, c.d, lanes, every);
+            return cudaGetLastError();
+        }
+        const int chunk = kScanThreads / lanes * ForwardRun<typename K::In, K::CHAN>::R;
+        return launch_clusters(scan_split_kernel<typename K::In, typename K::Out, K::CHAN, K::VEC>, units,
+                               ranks_of(units, a.n_tokens, chunk), s, a, c.heads, units, c.d, lanes, every);
     });
 }
 
