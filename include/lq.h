@@ -438,15 +438,17 @@ typedef struct lq_scan_config {
 
 typedef struct lq_scan_args {
     int32_t n_tokens;          /* T, >= 0                                         */
-    int32_t reserved;          /* must be 0                                       */
+    int32_t zero_past;         /* rows of the outputs and of the gradients of v, g
+                                  and beta past a length: 0 left as they are,
+                                  1 set to zero                                   */
     const void *v;             /* in_dtype [T][batch][heads][d], any strides      */
     const float *g;            /* f32 [T][batch][heads] or [..][d]: log alpha,
                                   <= 0 in ordinary use (-inf empties the state)   */
     const float *beta;         /* f32 [T][batch][heads]; NULL: 1                  */
     const float *h0;           /* f32 [batch][heads][d]: start; NULL: zero        */
     const int32_t *lengths;    /* int32 [batch]: tokens of each sequence, clamped
-                                  to 0..T; NULL: T.  Tokens past a length are
-                                  neither read nor written                        */
+                                  to 0..T; NULL: T.  Tokens past a length affect
+                                  nothing, whatever their rows hold               */
     void *out;                 /* out_dtype [T][batch][heads][d]; NULL: not wanted*/
     float *h_last;             /* f32 [batch][heads][d]: state after the last
                                   token (h0 where there is none); may be h0;

@@ -757,8 +757,8 @@ cudaError_t launch_t(const DecodeArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t make_codes_map(void *map_out, const int8_t *codes, int d, int units) {
-    // the driver's entry point, looked up once (first callers serialized)
+// looked up once (first callers serialized)
+cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out) {
     static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> entry{nullptr};
     static std::mutex lookup;
     PFN_cuTensorMapEncodeTiled_v12000 encode = entry.load(std::memory_order_acquire);
@@ -775,6 +775,14 @@ cudaError_t make_codes_map(void *map_out, const int8_t *codes, int d, int units)
             entry.store(encode, std::memory_order_release);
         }
     }
+    *out = encode;
+    return cudaSuccess;
+}
+
+cudaError_t make_codes_map(void *map_out, const int8_t *codes, int d, int units) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const cudaError_t e = tensor_map_encoder(&encode);
+    if (e != cudaSuccess) return e;
     const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)units * (cuuint64_t)d};
     const cuuint64_t strides[1] = {(cuuint64_t)d};
     const cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)d};

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -131,6 +132,9 @@ struct TokenPrefillArgs {
     int heads;
     int32_t *fill;
 };
+
+// The driver's tensor-map encoder.
+cudaError_t tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000 *out);
 
 // Encode the tensor map the windowed decode uses to load one unit's INT8 tile
 // (d x d, 128- or 64-byte swizzle) from `codes` ([units][d][d]).  Host only.

@@ -9,11 +9,10 @@
 namespace lq {
 
 // Tokens between two checkpoints of the gated scan: what one CTA of the
-// backward pass takes at a time.
-int scan_checkpoint_tokens(int d);
+// backward pass takes in a step.
+int scan_checkpoint_tokens(const lq_scan_config &c);
 
-// `vec`: every pointer and stride of the call lets a thread move eight
-// channels with 16-byte accesses, and d is a multiple of 8.
+// `vec`: every row of every tensor of the call is whole, aligned pieces of 16 bytes.
 cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, bool vec, cudaStream_t s);
 cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a, const lq_scan_grads &g, bool vec,
                                  cudaStream_t s);

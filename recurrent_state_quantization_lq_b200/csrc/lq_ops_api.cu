@@ -26,11 +26,21 @@ const char *why_not(const lq_scan_config *c) {
     return nullptr;
 }
 
-// Whether each row of a tensor lets a thread move eight channels with 16-byte accesses.
-bool rows_of_16_bytes(const void *p, const lq_strides &s, size_t e) {
+// A tensor [T][batch][heads][d] of one call.
+struct Extent {
+    int64_t T, B, H;
+    int d;
+};
+
+// Whether every row of a tensor is whole, aligned pieces of 16 bytes, and its
+// rows are apart (as a tensor map wants them).
+bool rows_of_16_bytes(const void *p, const lq_strides &s, const Extent &x, size_t e) {
     if (p == nullptr) return true;
-    const int64_t m = (int64_t)(16 / e);
-    return aligned(p, 16) && s.token % m == 0 && s.seq % m == 0 && s.head % m == 0;
+    auto fits = [&](int64_t n, int64_t stride) {
+        const int64_t bytes = stride * (int64_t)e;
+        return n <= 1 || (bytes > 0 && bytes % 16 == 0 && bytes < (1LL << 40));
+    };
+    return aligned(p, 16) && x.d * e % 16 == 0 && fits(x.T, s.token) && fits(x.B, s.seq) && fits(x.H, s.head);
 }
 
 // Whether two elements of an output could have one address for want of a stride.
@@ -41,15 +51,16 @@ bool strides_cover(const void *p, const lq_strides &s, int64_t T, int64_t B, int
 const char *why_not(const lq_scan_config &c, const lq_scan_args *a, bool *vec) {
     if (a == nullptr) return "args is NULL";
     if (a->n_tokens < 0) return "negative n_tokens";
-    if (a->reserved != 0) return "reserved must be 0";
+    if (a->zero_past != 0 && a->zero_past != 1) return "zero_past must be 0 or 1";
     if (a->n_tokens > 0 && (a->v == nullptr || a->g == nullptr)) return "NULL v or g";
     if (!aligned(a->v, element(c.in_dtype)) || !aligned(a->out, element(c.out_dtype)) || !aligned(a->g, 4) ||
         !aligned(a->beta, 4) || !aligned(a->h0, 4) || !aligned(a->h_last, 4) || !aligned(a->checkpoints, 4) ||
         !aligned(a->lengths, 4))
         return "a pointer is not aligned to its element";
     const bool chan = c.gate == LQ_GATE_CHANNEL;
-    *vec = c.d % 8 == 0 && rows_of_16_bytes(a->v, a->v_stride, element(c.in_dtype)) &&
-           (!chan || rows_of_16_bytes(a->g, a->g_stride, 4)) && aligned(a->h0, 16) && aligned(a->checkpoints, 16);
+    const Extent x{a->n_tokens, c.batch, c.heads, c.d};
+    *vec = c.d % 4 == 0 && rows_of_16_bytes(a->v, a->v_stride, x, element(c.in_dtype)) &&
+           (!chan || rows_of_16_bytes(a->g, a->g_stride, x, 4)) && aligned(a->h0, 16) && aligned(a->checkpoints, 16);
     return nullptr;
 }
 
@@ -102,7 +113,7 @@ size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t n_token
         fail(LQ_ERR_INVALID_ARG, why);
         return 0;
     }
-    const size_t every = (size_t)lq::scan_checkpoint_tokens(cfg->d);
+    const size_t every = (size_t)lq::scan_checkpoint_tokens(*cfg);
     return ((size_t)n_tokens + every - 1) / every * (size_t)cfg->batch * (size_t)cfg->heads * (size_t)cfg->d * 4;
 }
 
@@ -113,7 +124,8 @@ lq_status lq_gated_scan(const lq_scan_config *cfg, const lq_scan_args *args, voi
     if (const char *why = why_not(*cfg, args, &vec)) return fail(LQ_ERR_INVALID_ARG, why);
     if (!strides_cover(args->out, args->out_stride, args->n_tokens, cfg->batch, cfg->heads))
         return fail(LQ_ERR_INVALID_ARG, "an output dimension has stride 0");
-    vec = vec && rows_of_16_bytes(args->out, args->out_stride, element(cfg->out_dtype)) && aligned(args->h_last, 16);
+    const Extent x{args->n_tokens, cfg->batch, cfg->heads, cfg->d};
+    vec = vec && rows_of_16_bytes(args->out, args->out_stride, x, element(cfg->out_dtype)) && aligned(args->h_last, 16);
     const cudaError_t e = lq::launch_scan_forward(*cfg, *args, vec, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LQ_OK : cuda_fail(e, "launching the scan kernel");
 }
@@ -136,9 +148,10 @@ lq_status lq_gated_scan_backward(const lq_scan_config *cfg, const lq_scan_args *
         !strides_cover(grads->grad_g, grads->grad_g_stride, T, B, H) ||
         !strides_cover(grads->grad_beta, grads->grad_beta_stride, T, B, H))
         return fail(LQ_ERR_INVALID_ARG, "an output dimension has stride 0");
-    vec = vec && rows_of_16_bytes(grads->grad_out, grads->grad_out_stride, element(cfg->out_dtype)) &&
-          rows_of_16_bytes(grads->grad_v, grads->grad_v_stride, element(cfg->in_dtype)) &&
-          (cfg->gate != LQ_GATE_CHANNEL || rows_of_16_bytes(grads->grad_g, grads->grad_g_stride, 4));
+    const Extent x{T, B, H, cfg->d};
+    vec = vec && rows_of_16_bytes(grads->grad_out, grads->grad_out_stride, x, element(cfg->out_dtype)) &&
+          rows_of_16_bytes(grads->grad_v, grads->grad_v_stride, x, element(cfg->in_dtype)) &&
+          (cfg->gate != LQ_GATE_CHANNEL || rows_of_16_bytes(grads->grad_g, grads->grad_g_stride, x, 4));
     const cudaError_t e = lq::launch_scan_backward(*cfg, *args, *grads, vec, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LQ_OK : cuda_fail(e, "launching the scan's backward kernel");
 }

@@ -34,8 +34,17 @@ __device__ __forceinline__ void widen8(const Raw8<float> &r, float *f) {
     f[4] = r.hi.x; f[5] = r.hi.y; f[6] = r.hi.z; f[7] = r.hi.w;
 }
 
-// VEC: p is 16-byte aligned and all eight channels exist.  Otherwise the first
-// n (0..8) channels are read one by one and the rest are zero.
+// The same as four pairs.
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T> &r, float2 *f) {
+    float x[8];
+    widen8(r, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+
+// The first n (1..8) channels of a row; the rest are zero.  VEC: p is 16-byte
+// aligned and n whole pieces of 16 bytes (8 BF16 channels; 4 or 8 FP32).
 template <bool VEC>
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, Raw8<__nv_bfloat16> &r) {
     if constexpr (VEC) {
@@ -53,7 +62,7 @@ template <bool VEC>
 __device__ __forceinline__ void load8(const float *p, int n, Raw8<float> &r) {
     if constexpr (VEC) {
         r.lo = __ldg(reinterpret_cast<const float4 *>(p));
-        r.hi = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        r.hi = n > 4 ? __ldg(reinterpret_cast<const float4 *>(p) + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
         float f[8];
 #pragma unroll
@@ -80,13 +89,25 @@ template <bool VEC>
 __device__ __forceinline__ void store8(float *p, int n, const float *f) {
     if constexpr (VEC) {
         reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        if (n > 4) reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = f[i];
     }
 }
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T *p, int n, const float2 *f) {
+    const float x[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    store8<VEC>(p, n, x);
+}
+
+// Two FP32 operations in one instruction (sm_100a's packed pairs); each half
+// rounds as the scalar operation does.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // Lanes that share a row of d channels, eight each: a power of two, 1..32.
 __host__ __device__ inline int row_lanes(int d) {

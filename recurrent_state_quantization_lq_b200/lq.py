@@ -69,7 +69,7 @@ class ScanConfig(ctypes.Structure):
 
 
 class ScanArgs(ctypes.Structure):
-    _fields_ = [("n_tokens", ctypes.c_int32), ("reserved", ctypes.c_int32)] + \
+    _fields_ = [("n_tokens", ctypes.c_int32), ("zero_past", ctypes.c_int32)] + \
         [(n, ctypes.c_void_p) for n in ("v", "g", "beta", "h0", "lengths", "out", "h_last", "checkpoints")] + \
         [(n, Strides) for n in ("v_stride", "g_stride", "beta_stride", "out_stride")]
 
@@ -286,7 +286,8 @@ def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None,
     out_dtype = out.dtype if out is not None else out_dtype or v.dtype
     cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
     if out is None and want_out:
-        out = (torch.empty_like if lengths is None else torch.zeros_like)(v, dtype=out_dtype)
+        out = torch.empty_like(v, dtype=out_dtype)
+        args.zero_past = 1
     if h_last is None:
         h_last = torch.empty(v.shape[1:], dtype=torch.float32, device=v.device)
     args.h0 = _tensor(h0, "h0", v, torch.float32, v.shape[1:])
@@ -314,7 +315,12 @@ def gated_scan_backward(grad_out, v, g, beta=None, *, checkpoints, grad_last=Non
                                        grad_h0=grad_h0)
     out_dtype = v.dtype if grad_out is None else grad_out.dtype
     cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
-    new = torch.empty_like if lengths is None else torch.zeros_like
+    new = torch.empty_like
+    if lengths is not None:                    # rows past a length: by the kernel, unless a given tensor keeps its own
+        if grad_v is None and grad_g is None and grad_beta is None:
+            args.zero_past = 1
+        else:
+            new = torch.zeros_like
     grad_v = new(v) if grad_v is None else grad_v
     grad_g = new(g) if grad_g is None else grad_g
     if beta is not None and grad_beta is None:

@@ -40,7 +40,7 @@ def test_scan_configs_refused(field, value):
     assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args()), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw,word", [({"n_tokens": -1}, "negative"), ({"reserved": 1}, "reserved"), ({"v": None}, "NULL"),
+@pytest.mark.parametrize("kw,word", [({"n_tokens": -1}, "negative"), ({"zero_past": 2}, "zero_past"), ({"v": None}, "NULL"),
                                      ({"g": None}, "NULL"), ({"v": P + 1}, "aligned"), ({"g": P + 2}, "aligned"),
                                      ({"lengths": P + 1}, "aligned"), ({"h0": P + 2}, "aligned"),
                                      ({"checkpoints": P + 3}, "aligned"), ({"beta": P + 1}, "aligned")])
