@@ -14,22 +14,26 @@
 // Layout of the work.  A thread holds eight channels of a row (lq_vec8.cuh);
 // row_lanes(d) adjacent lanes hold a row.  A cluster of CTAs takes one unit:
 // `ranks` CTAs x (rows of lanes) x R consecutive tokens a step.
-//   Pass one: each row runs its R tokens from zero; the rows' maps are composed
-//     over the warp by shuffles and left in shared memory.
-//   The composer, a warp of its own, composes the eight warps' maps, exchanges
-//     the CTA's map with the cluster through distributed shared memory and
-//     leaves the true state before each warp's tokens.
-//   Pass two: each row runs its tokens, still in shared memory, from their true
-//     start and stores the results.
-// The workers take pass two of a step after pass one of the next one, so that
-// the composer's chain of latencies (about 1500 cycles in a cluster) costs no
-// time; a third kind of warp, the loader, keeps the tokens of up to three steps
-// in flight or in use.  Measured without that split, with every warp waiting
-// for the maps of its own step, a step of 32 KB took 6400 cycles (8200 in a
-// cluster) where the memory needs 5800 for two CTAs.
+//   Pass one: each row runs its R tokens from zero and leaves its map in shared
+//     memory (rows shorter than half a warp first compose theirs by shuffles).
+//   The composer, a warp of its own, composes these maps, exchanges the CTA's
+//     map with the cluster through distributed shared memory and leaves the true
+//     state before each row's tokens.
+//   Pass two: the results from the true start.
+// Another warp, the loader, keeps the tokens of up to three steps in flight or
+// in use and raises the gates.
+//   Forward, pass two runs the row's tokens, still in shared memory, again, and
+// comes after pass one of the next step, so that the composer's chain of
+// latencies (about 1500 cycles in a cluster) costs no time.  Without that
+// split, every warp waiting for the maps of its own step, a step of 64 KB of an
+// SM took 6400 cycles (8200 in a cluster) where the memory needs 5800.
+//   Backward there are twice the results a token and the instructions count:
+// pass one keeps its local results in registers and pass two corrects them by
+// what enters the row; the two CTAs of an SM cover each other's waits.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lq_ops.h"
 #include "lq_kernels.h"
@@ -39,20 +43,24 @@ namespace cg = cooperative_groups;
 
 namespace lq {
 
-constexpr int kWorkers = 256;                    // threads that run tokens: warps 0..7
-constexpr int kWorkerWarps = kWorkers / 32;
-constexpr int kSplitThreads = kWorkers + 64;     // and the composer (warp 8) and the loader (warp 9)
+// Warps that run tokens, beside the composer and the loader.  Forward, three
+// stages of tokens and two steps' maps of two CTAs just fit an SM's shared
+// memory; backward, two CTAs of eight warps leave a thread 128 registers.
+constexpr int kForwardWarps = 7;
+constexpr int kBackwardWarps = 6;
 constexpr int kStages = 3;                       // steps whose tokens are in shared memory
 constexpr int kMostRanks = 8;                    // CTAs of a cluster (the portable size)
 constexpr int kRowsThreads = 256;                // of the kernel for a few tokens
 
-// Consecutive tokens that a row of lanes takes in a step: as many as let two
-// CTAs' stages share an SM.
+// Consecutive tokens that a row of lanes takes in a step: as many as the two
+// CTAs' stages have room for.
 constexpr int forward_run(bool bf16, bool chan) { return chan ? 2 : bf16 ? 8 : 4; }
 constexpr int backward_run(bool bf16, bool chan) { return bf16 && !chan ? 4 : 2; }
 
+// (a multiple of every forward_run of the same types, so that a checkpoint
+// falls on the start of a row's tokens there)
 int scan_checkpoint_tokens(const lq_scan_config &c) {
-    return kWorkers / row_lanes(c.d) * backward_run(c.in_dtype == LQ_DTYPE_BF16, c.gate == LQ_GATE_CHANNEL);
+    return 32 * kBackwardWarps / row_lanes(c.d) * backward_run(c.in_dtype == LQ_DTYPE_BF16, c.gate == LQ_GATE_CHANNEL);
 }
 
 namespace {
@@ -96,57 +104,58 @@ __device__ __forceinline__ int64_t row_of(const lq_strides &s, const Unit &w, in
     return (int64_t)t * s.token + (int64_t)w.b * s.seq + (int64_t)w.h * s.head;
 }
 
-// The gates of a thread's eight channels, in pairs (scalar gate: one pair of equal values).
+// The gates of a thread's eight channels: four pairs, or one value for all.
 template <bool CHAN>
 struct Gates {
-    static constexpr int N = CHAN ? 4 : 1;
-    float2 a[N];
-    __device__ __forceinline__ float2 operator[](int i) const { return a[CHAN ? i : 0]; }
+    float2 a[4];
+    __device__ __forceinline__ float2 operator[](int i) const { return a[i]; }
     __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = make_float2(x, x);
+        for (int i = 0; i < 4; ++i) a[i] = make_float2(x, x);
     }
     template <bool VEC>
     __device__ __forceinline__ void load(const float *p, int n) {   // log gates, as they lie in memory
-        if constexpr (CHAN) {
-            Raw8<float> r;
-            load8<VEC>(p, n, r);
-            widen8(r, a);
-        } else {
-            fill(__ldg(p));
-        }
+        Raw8<float> r;
+        load8<VEC>(p, n, r);
+        widen8(r, a);
     }
     __device__ __forceinline__ void exponentiate() {
-        if constexpr (CHAN) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) a[i] = gates_of(a[i]);
-        } else {
-            fill(gate_of(a[0].x));
-        }
+        for (int i = 0; i < 4; ++i) a[i] = gates_of(a[i]);
     }
     __device__ __forceinline__ void times(const Gates &b) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) a[i] = mul2(a[i], b.a[i]);
+        for (int i = 0; i < 4; ++i) a[i] = mul2(a[i], b.a[i]);
     }
     // the gates `o` lanes before (after) this one
     __device__ __forceinline__ Gates before(int o) const {
         Gates r;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r.a[i].x = __shfl_up_sync(0xffffffffu, a[i].x, o);
-            r.a[i].y = CHAN ? __shfl_up_sync(0xffffffffu, a[i].y, o) : r.a[i].x;
-        }
+        for (int i = 0; i < 4; ++i)
+            r.a[i] = make_float2(__shfl_up_sync(0xffffffffu, a[i].x, o), __shfl_up_sync(0xffffffffu, a[i].y, o));
         return r;
     }
     __device__ __forceinline__ Gates after(int o) const {
         Gates r;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r.a[i].x = __shfl_down_sync(0xffffffffu, a[i].x, o);
-            r.a[i].y = CHAN ? __shfl_down_sync(0xffffffffu, a[i].y, o) : r.a[i].x;
-        }
+        for (int i = 0; i < 4; ++i)
+            r.a[i] = make_float2(__shfl_down_sync(0xffffffffu, a[i].x, o), __shfl_down_sync(0xffffffffu, a[i].y, o));
         return r;
     }
+};
+template <>
+struct Gates<false> {
+    float a;
+    __device__ __forceinline__ float2 operator[](int) const { return make_float2(a, a); }
+    __device__ __forceinline__ void fill(float x) { a = x; }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float *p, int) {
+        a = __ldg(p);
+    }
+    __device__ __forceinline__ void exponentiate() { a = gate_of(a); }
+    __device__ __forceinline__ void times(const Gates &b) { a *= b.a; }
+    __device__ __forceinline__ Gates before(int o) const { return Gates{__shfl_up_sync(0xffffffffu, a, o)}; }
+    __device__ __forceinline__ Gates after(int o) const { return Gates{__shfl_down_sync(0xffffffffu, a, o)}; }
 };
 
 __device__ __forceinline__ float2 pair_before(float2 x, int o) {
@@ -160,14 +169,19 @@ __device__ __forceinline__ float2 pair_after(float2 x, int o) {
 
 // One tensor's rows [token][sequence][head][d] as the tensor-map copies see
 // them: a box is some consecutive tokens of one (sequence, head).
-constexpr int kMostBox = 256;       // tokens a box may have
 struct RowMap {
     CUtensorMap map;
 };
+// Tokens of a box: the step's tokens of a CTA (three or seven times a power of
+// two), halved until a box may have them (256).
+__host__ __device__ inline int box_of(int tokens) {
+    while (tokens > 256) tokens /= 2;
+    return tokens;
+}
 
 __device__ __forceinline__ void bring_boxes(unsigned char *base, const RowMap &m, const Unit &w, int t_first, int tokens,
                                             int row_bytes, uint64_t *bar) {
-    const int box = min(tokens, kMostBox);
+    const int box = box_of(tokens);
     for (int t = 0; t < tokens; t += box)
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
@@ -192,18 +206,22 @@ __device__ __forceinline__ void bring_row(unsigned char *base, int pitch, const 
         }
     }
 }
-// Eight channels of a token in shared memory, as pairs (where fewer exist, what
-// follows them is read too).
+// Eight channels of a token in shared memory (where fewer exist, what follows
+// them is read too), as they lie there or as pairs.
 template <typename T>
-__device__ __forceinline__ void read_shared(const unsigned char *base, int pitch, int token, int c0, float2 *x) {
+__device__ __forceinline__ void read_shared(const unsigned char *base, int pitch, int token, int c0, Raw8<T> &r) {
     const T *q = reinterpret_cast<const T *>(base) + token * pitch + c0;
-    Raw8<T> r;
     if constexpr (sizeof(T) == 2) {
         r.w = *reinterpret_cast<const uint4 *>(q);
     } else {
         r.lo = reinterpret_cast<const float4 *>(q)[0];
         r.hi = reinterpret_cast<const float4 *>(q)[1];
     }
+}
+template <typename T>
+__device__ __forceinline__ void read_shared(const unsigned char *base, int pitch, int token, int c0, float2 *x) {
+    Raw8<T> r;
+    read_shared(base, pitch, token, c0, r);
     widen8(r, x);
 }
 __device__ __forceinline__ void read_shared(const float *q, float2 *x) {
@@ -223,36 +241,54 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// The workers and the composer meet.
-__device__ __forceinline__ void maps_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers + 32) : "memory"); }
+// A named barrier of some of a CTA's warps.
+template <int ID, int THREADS>
+__device__ __forceinline__ void meet() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
 
-// The shared memory of one CTA: the stages (the tensors, then a pair (log gate,
-// beta) a token) and, twice by the parity of the step, the warps' maps.
-// BYTES: of a channel of a token; DIRS: maps a warp leaves (1 forward, 2 backward).
-template <int BYTES, bool CHAN, int DIRS>
+// The stages of one CTA in shared memory: up to three tensors, then a pair (log
+// gate or alpha, beta) a token, then (backward) the state before the tokens.
+// NW: workers' warps; B0, B1, B2: bytes of a channel of the tensors.
+template <int NW_, int B0, int B1, int B2, bool CHAN, bool BACK>
 struct Space {
-    int tokens, dp;
-    __host__ __device__ Space(int n_tokens, int d) : tokens(n_tokens), dp((d + 7) / 8 * 8) {}
-    // rows that a tensor map fills are packed; the last thread of the last row may read 16 bytes past them
-    __host__ __device__ int scalars() const { return (tokens * dp * BYTES + 16 + 127) / 128 * 128; }
-    __host__ __device__ int stage() const { return (scalars() + tokens * 8 + 127) / 128 * 128; }
-    __host__ __device__ int map() const { return kWorkerWarps * (DIRS * dp + (CHAN ? dp : 4)); }   // floats
-    __host__ __device__ int peer() const { return dp + (CHAN ? dp : 4); }                          // floats
+    static constexpr int NW = NW_;
+    int tokens, dp, rows;
+    __host__ __device__ Space(int d, int lanes, int run)
+        : tokens(32 * NW / lanes * run), dp((d + 7) / 8 * 8), rows(32 * NW / lanes) {}
+    __host__ __device__ static int up(int bytes) { return (bytes + 127) / 128 * 128; }
+    // where a tensor starts (a tensor map's copies want 128 bytes), and what follows them
+    __host__ __device__ int second() const { return up(tokens * dp * B0); }
+    __host__ __device__ int third() const { return second() + up(tokens * dp * B1); }
+    __host__ __device__ int scalars() const { return third() + up(tokens * dp * B2); }
+    __host__ __device__ int mark() const { return up(scalars() + tokens * 8); }
+    __host__ __device__ int stage() const { return mark() + (BACK ? up(dp * 4) : 0); }
+    // In floats, the maps of a step.  Forward, of the warps: H [NW][dp], A [NW][dp
+    // or 4].  Backward, of the rows: H, E [rows][dp], A, B [rows][dp or 1] (A:
+    // the gates' product from the group's first row on, B: from its last).
+    __host__ __device__ int gate_row() const { return CHAN ? dp : BACK ? 1 : 4; }
+    __host__ __device__ int E() const { return rows * dp; }
+    __host__ __device__ int A() const { return BACK ? 2 * rows * dp : NW * dp; }
+    __host__ __device__ int B() const { return A() + rows * gate_row(); }
+    __host__ __device__ int map() const { return BACK ? (B() + rows * gate_row() + 3) / 4 * 4 : A() + NW * gate_row(); }
+    __host__ __device__ int maps() const { return (BACK ? 1 : 2) * map(); }
+    // a CTA's map as its peers see it: H or E [dp], then A [dp, or 4 equal]
+    __host__ __device__ int peer() const { return dp + (CHAN ? dp : 4); }
     __host__ __device__ int bytes(int ranks) const {
-        return kStages * stage() + 2 * map() * 4 + (ranks > 1 ? 2 * ranks * peer() * 4 : 0);
+        return kStages * stage() + maps() * 4 + (ranks > 1 ? 2 * ranks * peer() * 4 : 0);
     }
 };
 
 // Barriers of a CTA.
 struct Bars {
-    uint64_t full[kStages];      // the loader's copies of a stage have landed
-    uint64_t empty[kStages];     // the eight warps have read a stage
+    uint64_t full[kStages];      // a stage's tokens are there
+    uint64_t empty[kStages];     // the workers' warps have read a stage
     uint64_t peer[2];            // the cluster's maps of a step are here
 };
-__device__ __forceinline__ void init_bars(Bars &b) {
+__device__ __forceinline__ void init_bars(Bars &b, int workers) {
     for (int i = 0; i < kStages; ++i) {
         mbar_init(&b.full[i], 1 + 32);
-        mbar_init(&b.empty[i], kWorkerWarps);
+        mbar_init(&b.empty[i], workers);
     }
     mbar_init(&b.peer[0], 1);
     mbar_init(&b.peer[1], 1);
@@ -277,7 +313,12 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t local, int rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
-// Store four values in a peer's shared memory and count their bytes at the peer's barrier.
+// Store values in a peer's shared memory and count their bytes at the peer's barrier.
+__device__ __forceinline__ void peer_store(uint32_t dst, float x, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+                 "r"(__float_as_uint(x)), "r"(bar)
+                 : "memory");
+}
 __device__ __forceinline__ void peer_store(uint32_t dst, float4 x, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
                  "r"(__float_as_uint(x.x)), "r"(__float_as_uint(x.y)), "r"(__float_as_uint(x.z)),
@@ -327,16 +368,14 @@ __device__ __forceinline__ void store4(float *p, int n, const float4 &x) {
     if (n > 3) p[3] = x.w;
 }
 
-// The composer's work.  A lane owns channels 4 q .. 4 q + 3 for q = lane and
-// lane + 32.  A step's maps are [H][kWorkerWarps][dp] (backward: then E), then
-// A [kWorkerWarps][dp or 4].  BACK: the cluster's order runs from its last CTA
-// to its first.
-template <bool CHAN, bool BACK>
+// The forward composer's work.  A lane owns channels 4 q .. 4 q + 3 for q = lane
+// and lane + 32.
+template <int NW, bool CHAN>
 struct Composer {
     float *peers;            // [2][ranks][H dp, A (dp, or 4 equal)]
     uint64_t *bars;          // [2]
     int ranks, rank, dp;
-    float4 carry[2];         // what enters the step
+    float4 carry[2];         // the state before the step
     bool alive = true;       // a wait that ran out is the last one, and what follows it is NaN
 
     __device__ __forceinline__ int owned() const { return (dp / 4 - (int)(threadIdx.x % 32) + 31) / 32; }
@@ -344,8 +383,8 @@ struct Composer {
         return Map4{*reinterpret_cast<const float4 *>(A + k * (CHAN ? dp : 4) + (CHAN ? 4 * q : 0)),
                     *reinterpret_cast<const float4 *>(H + k * dp + 4 * q)};
     }
-    // Replace the warps' maps of `step` by what enters each warp.  Every CTA
-    // stores its map in all CTAs and waits at its own barrier for everybody's:
+    // Replace the warps' maps of `step` by the states before their tokens.  Every
+    // CTA stores its map in all CTAs and waits at its own barrier for everybody's:
     // unlike a cluster barrier this waits for no store to global memory.  A CTA
     // stores its map of step s + 2 only after it has those of s + 1, whose
     // senders had read step s.
@@ -355,10 +394,10 @@ struct Composer {
             if (lane == 0) mbar_arrive_expect_tx(bars + p, (uint32_t)(ranks * size * 4));
             for (int j = 0; j < owned(); ++j) {
                 const int q = lane + 32 * j;
-                Map4 all = map(H, A, BACK ? kWorkerWarps - 1 : 0, q);
+                Map4 all = map(H, A, 0, q);
 #pragma unroll
-                for (int k = 1; k < kWorkerWarps; ++k) {
-                    const Map4 m = map(H, A, BACK ? kWorkerWarps - 1 - k : k, q);
+                for (int k = 1; k < NW; ++k) {
+                    const Map4 m = map(H, A, k, q);
                     all.H = apply(m, all.H);
                     all.A = times4(all.A, m.A);
                 }
@@ -379,20 +418,27 @@ struct Composer {
             if (ranks > 1) {
                 if (!alive) carry[j] = four(nanf(""));
 #pragma unroll
-                for (int i = 0; i < kMostRanks; ++i) {
-                    if (i >= ranks) break;
-                    const int r = BACK ? ranks - 1 - i : i;
+                for (int r = 0; r < kMostRanks; ++r) {
+                    if (r >= ranks) break;
                     const float *m = peers + (p * ranks + r) * size;
                     if (r == rank) x = carry[j];
                     carry[j] = apply(map(m, m + dp, 0, q), carry[j]);
                 }
             }
+            // four maps are read before the first is replaced: one after another
+            // their latencies would add up
 #pragma unroll
-            for (int i = 0; i < kWorkerWarps; ++i) {
-                const int k = BACK ? kWorkerWarps - 1 - i : i;
-                const Map4 m = map(H, A, k, q);
-                *reinterpret_cast<float4 *>(H + k * dp + 4 * q) = x;
-                x = apply(m, x);
+            for (int k = 0; k < NW; k += 4) {
+                Map4 m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (k + i < NW) m[i] = map(H, A, k + i, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (k + i >= NW) break;
+                    *reinterpret_cast<float4 *>(H + (k + i) * dp + 4 * q) = x;
+                    x = apply(m[i], x);
+                }
             }
             if (ranks == 1) carry[j] = x;
         }
@@ -441,24 +487,25 @@ __global__ void __launch_bounds__(kRowsThreads) scan_rows_kernel(lq_scan_args a,
 }
 
 template <typename InT, bool CHAN>
-using ForwardSpace = Space<(int)sizeof(InT) + (CHAN ? 4 : 0), CHAN, 1>;
+using ForwardSpace = Space<kForwardWarps, (int)sizeof(InT), CHAN ? 4 : 0, 0, CHAN, false>;
 
 template <typename InT, typename OutT, bool CHAN, bool VEC>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+__global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
     scan_forward_kernel(lq_scan_args a, const __grid_constant__ RowMap map_v, const __grid_constant__ RowMap map_g,
                         int heads, int units, int d, int lanes, int every) {
     constexpr int R = forward_run(sizeof(InT) == 2, CHAN);
+    constexpr int NW = kForwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Bars bars;
-    const int rows = kWorkers / lanes, chunk = rows * R;
-    const ForwardSpace<InT, CHAN> space(chunk, d);
+    const int rows = 32 * NW / lanes, chunk = rows * R;
+    const ForwardSpace<InT, CHAN> space(d, lanes, R);
     const int dp = space.dp, pitch = VEC ? d : dp;
-    const int gates_at = chunk * pitch * (int)sizeof(InT);          // the log gates of channels in a stage
+    const int gates_at = space.second();                            // the log gates of channels in a stage
     float *maps = reinterpret_cast<float *>(smem + kStages * space.stage());
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    if (tid == 0) init_bars(bars);
+    if (tid == 0) init_bars(bars, NW);
     __syncthreads();
     if (ranks > 1) cluster.sync();
 
@@ -468,7 +515,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const float *pg = a.g + row_of(a.g_stride, w, 0);
     const float *pb = a.beta != nullptr ? a.beta + row_of(a.beta_stride, w, 0) : nullptr;
 
-    if (warp == kWorkerWarps + 1) {                  // the loader
+    if (warp == NW + 1) {                  // the loader
         Turn turn;
         for (int s = 0; s < steps; ++s, turn.next()) {
             const int t_cta = s * stride + rank * chunk, live = min(max(w.len - t_cta, 0), chunk);
@@ -490,8 +537,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
             cp_async_arrive(full);
         }
-    } else if (warp == kWorkerWarps) {               // the composer
-        Composer<CHAN, false> composer{maps + 2 * space.map(), bars.peer, ranks, rank, dp};
+    } else if (warp == NW) {               // the composer
+        Composer<NW, CHAN> composer{maps + space.maps(), bars.peer, ranks, rank, dp};
         const int64_t state = (int64_t)w.u * d;
         for (int j = 0; j < 2; ++j) {
             const int c = 4 * (lane + 32 * j);
@@ -499,19 +546,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         }
         for (int s = 0; s < steps; ++s) {
             float *H = maps + (s & 1) * space.map();
-            maps_barrier();
-            composer.run(s, H, H + kWorkerWarps * dp);
+            meet<1, 32 * NW + 32>();
+            composer.run(s, H, H + NW * dp);
         }
-        maps_barrier();
+        meet<1, 32 * NW + 32>();
         if (rank == 0 && a.h_last != nullptr)
             for (int j = 0; j < 2; ++j) {
                 const int c = 4 * (lane + 32 * j);
                 store4(a.h_last + state + c, d - c, composer.carry[j]);
             }
     } else {                                         // the workers
-        const int c0 = (lane % lanes) * 8, row = tid / lanes;
+        const int in_row = lane & (lanes - 1), c0 = in_row * 8, row = tid / lanes;
         const bool on = c0 < d;
-        const int n = on ? min(8, d - c0) : 0;
+        const int n = on ? min(8, d - c0) : 0, cr = on ? c0 : 0;     // (lanes past d run with others' channels)
+        const int last_row = (tid | 31) / lanes;                     // of the warp
         auto bring = [&](int s, int stage) {
             const int t_row = s * stride + rank * chunk + row * R, live = min(max(w.len - t_row, 0), R);
             unsigned char *base = smem + stage * space.stage();
@@ -523,6 +571,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             for (int s = 0; s < kStages; ++s) bring(s, s);
         bool alive = true;           // a wait that ran out is the last one, and what follows it is NaN
         Turn one, two;               // the stages of pass one and pass two
+        // the row's first token is past_mark tokens past checkpoint `mark`, step after step
+        const int stride_marks = stride / every, stride_past = stride - stride_marks * every;
+        int mark = (rank * chunk + row * R) / every, past_mark = rank * chunk + row * R - mark * every;
         Gates<CHAN> A_before;        // of the step whose pass two is due: the map of its warp's rows before this one
         float2 H_before[4];
         for (int s = 0; s <= steps; ++s) {
@@ -533,33 +584,38 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 const int live = min(max(w.len - (s * stride + rank * chunk + row * R), 0), R);
                 unsigned char *base = smem + one.stage * space.stage();
                 float2 *sc = reinterpret_cast<float2 *>(base + space.scalars()) + row * R;
-                float *sH = maps + (s & 1) * space.map(), *sA = sH + kWorkerWarps * dp;
+                float *sH = maps + (s & 1) * space.map(), *sA = sH + NW * dp;
                 if (alive) alive = mbar_wait(&bars.full[one.stage], one.parity, kWaitBudgetCycles);
                 if (!alive) A.fill(nanf(""));
                 if (!CHAN) {                         // each gate is raised once, by one lane of its row
-                    for (int i = lane % lanes; i < live; i += lanes) sc[i].x = gate_of(sc[i].x);
+                    for (int i = in_row; i < live; i += lanes) sc[i].x = gate_of(sc[i].x);
                     __syncwarp();
                 }
+                // FULL: every row of the warp has R tokens (a straight line of code)
+                auto pass = [&](auto FULL) {
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    if (i >= live || !on) break;
-                    const float2 gb = sc[i];
-                    const float b = pb != nullptr ? gb.y : 1.0f;
-                    Gates<CHAN> gate;
-                    if constexpr (CHAN) {            // raised once: pass two finds alpha in its place
-                        float *g = reinterpret_cast<float *>(base + gates_at) + (row * R + i) * pitch + c0;
-                        read_shared(g, gate.a);
-                        gate.exponentiate();
-                        store8<true>(g, n, gate.a);
-                    } else {
-                        gate.fill(gb.x);
+                    for (int i = 0; i < R; ++i) {
+                        if (!FULL && (i >= live || !on)) break;
+                        const float2 gb = sc[i];
+                        const float b = pb != nullptr ? gb.y : 1.0f;
+                        Gates<CHAN> gate;
+                        if constexpr (CHAN) {        // raised once: pass two finds alpha in its place
+                            float *g = reinterpret_cast<float *>(base + gates_at) + (row * R + i) * pitch + cr;
+                            read_shared(g, gate.a);
+                            gate.exponentiate();
+                            if (on) store8<true>(g, n, gate.a);
+                        } else {
+                            gate.fill(gb.x);
+                        }
+                        float2 v[4];
+                        read_shared<InT>(base, pitch, row * R + i, cr, v);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) H[c] = fma2(gate[c], H[c], mul2(make_float2(b, b), v[c]));
+                        A.times(gate);
                     }
-                    float2 v[4];
-                    read_shared<InT>(base, pitch, row * R + i, c0, v);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) H[c] = fma2(gate[c], H[c], mul2(make_float2(b, b), v[c]));
-                    A.times(gate);
-                }
+                };
+                if (s * stride + rank * chunk + (last_row + 1) * R <= w.len) pass(std::true_type());
+                else pass(std::false_type());
                 for (int o = lanes; o < 32; o *= 2) {
                     const Gates<CHAN> before = A.before(o);
 #pragma unroll
@@ -572,43 +628,53 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 if (on && lane >= 32 - lanes) {
                     store8<true>(sH + warp * dp + c0, 8, H);
                     if constexpr (CHAN) store8<true>(sA + warp * dp + c0, 8, A.a);
-                    else if (c0 == 0) *reinterpret_cast<float4 *>(sA + warp * 4) = four(A.a[0].x);
+                    else if (c0 == 0) *reinterpret_cast<float4 *>(sA + warp * 4) = four(A.a);
                 }
                 A = A.before(lanes);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) H[c] = pair_before(H[c], lanes);
                 one.next();
             }
-            maps_barrier();          // the maps of step s are there, and the states of step s - 1
+            meet<1, 32 * NW + 32>();          // the maps of step s are there, and the states of step s - 1
             if (s > 0) {
                 const int t_row = (s - 1) * stride + rank * chunk + row * R, live = min(max(w.len - t_row, 0), R);
                 const unsigned char *base = smem + two.stage * space.stage();
                 const float2 *sc = reinterpret_cast<const float2 *>(base + space.scalars()) + row * R;
-                if (on && live > 0) {
-                    float2 h[4];
-                    read_shared(maps + ((s - 1) & 1) * space.map() + warp * dp + c0, h);
+                float2 h[4];
+                read_shared(maps + ((s - 1) & 1) * space.map() + warp * dp + cr, h);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (lane >= lanes) h[c] = fma2(A_before[c], h[c], H_before[c]);
-                    if (a.checkpoints != nullptr && t_row % every == 0)
-                        store8<VEC>(a.checkpoints + ((int64_t)(t_row / every) * units + w.u) * d + c0, n, h);
-                    if (a.out != nullptr) {
-                        OutT *po = static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t_row) + c0;
-#pragma unroll
-                        for (int i = 0; i < R; ++i, po += a.out_stride.token) {
-                            if (i >= live) break;
-                            const float2 gb = sc[i];
-                            const float b = pb != nullptr ? gb.y : 1.0f;
-                            Gates<CHAN> gate;
-                            if constexpr (CHAN) read_shared<float>(base + gates_at, pitch, row * R + i, c0, gate.a);
-                            else gate.fill(gb.x);
-                            float2 v[4];
-                            read_shared<InT>(base, pitch, row * R + i, c0, v);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) h[c] = fma2(gate[c], h[c], mul2(make_float2(b, b), v[c]));
-                            store8<VEC>(po, n, h);
-                        }
+                for (int c = 0; c < 4; ++c)
+                    if (lane >= lanes) h[c] = fma2(A_before[c], h[c], H_before[c]);
+                if (a.checkpoints != nullptr) {
+                    if (on && live > 0 && past_mark == 0)
+                        store8<VEC>(a.checkpoints + ((int64_t)mark * units + w.u) * d + c0, n, h);
+                    mark += stride_marks;
+                    past_mark += stride_past;
+                    if (past_mark >= every) {
+                        past_mark -= every;
+                        ++mark;
                     }
+                }
+                auto pass = [&](auto FULL) {
+                    OutT *po = static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t_row) + c0;
+#pragma unroll
+                    for (int i = 0; i < R; ++i, po += a.out_stride.token) {
+                        if (!FULL && (i >= live || !on)) break;
+                        const float2 gb = sc[i];
+                        const float b = pb != nullptr ? gb.y : 1.0f;
+                        Gates<CHAN> gate;
+                        if constexpr (CHAN) read_shared<float>(base + gates_at, pitch, row * R + i, cr, gate.a);
+                        else gate.fill(gb.x);
+                        float2 v[4];
+                        read_shared<InT>(base, pitch, row * R + i, cr, v);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) h[c] = fma2(gate[c], h[c], mul2(make_float2(b, b), v[c]));
+                        if (!FULL || on) store8<VEC>(po, n, h);
+                    }
+                };
+                if (a.out != nullptr) {
+                    if ((s - 1) * stride + rank * chunk + (last_row + 1) * R <= w.len) pass(std::true_type());
+                    else pass(std::false_type());
                 }
                 if (!VEC && s - 1 + kStages < steps) bring(s - 1 + kStages, two.stage);
                 if (CHAN) fence_proxy_async_smem();  // alpha was written where the next copy lands
@@ -634,10 +700,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 
 // Sums of N values over the lanes of a row, N a power of two up to the lanes:
 // at each of the first levels a lane hands half of its values over, so a value
-// costs about one shuffle.  The lane is left with the sum of value *index.
+// costs about one shuffle; a lane is left with the sum of one value.
 template <int N>
-__device__ __forceinline__ float sum_row(float (&x)[N], int lanes, int lane, int *index) {
-    int o = lanes / 2, at = 0;
+__device__ __forceinline__ float sum_row(float (&x)[N], int lanes, int lane) {
+    int o = lanes / 2;
 #pragma unroll
     for (int m = N / 2; m >= 1; m /= 2, o /= 2) {
         const bool high = (lane & o) != 0;
@@ -646,38 +712,47 @@ __device__ __forceinline__ float sum_row(float (&x)[N], int lanes, int lane, int
             const float keep = high ? x[i + m] : x[i], give = high ? x[i] : x[i + m];
             x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
-        at += high ? m : 0;
     }
     float s = x[0];
     for (; o >= 1; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    *index = at;
     return s;
+}
+// The value whose sum sum_row leaves with a lane.
+template <int N>
+__device__ __forceinline__ int sum_of(int lanes, int lane) {
+    int o = lanes / 2, at = 0;
+#pragma unroll
+    for (int m = N / 2; m >= 1; m /= 2, o /= 2) at += (lane & o) != 0 ? m : 0;
+    return at;
 }
 
 template <typename InT, typename OutT, bool CHAN>
-using BackwardSpace = Space<(int)sizeof(InT) + (int)sizeof(OutT) + (CHAN ? 4 : 0), CHAN, 2>;
+using BackwardSpace = Space<kBackwardWarps, (int)sizeof(InT), (int)sizeof(OutT), CHAN ? 4 : 0, CHAN, true>;
 
-// Steps run from the sequence's end.  Pass one also runs a row's tokens
-// backwards from zero (E); the composer starts a step's states from the CTA's
-// checkpoint, so only the gradient's maps cross the cluster; pass two runs the
-// states up and the gradients down and multiplies them.
+// Steps run from the sequence's end.  Pass one runs a row's tokens forwards from
+// zero (alpha h, H) and backwards from zero (D, E); the composer starts a step's
+// states from the CTA's checkpoint, so only the gradient's maps cross the
+// cluster.  With h what enters the row from before and X from behind, P_t the
+// product of its gates up to t and Q_t of those after t, pass two has
+//     alpha_t h_{t-1} = P_t h + its local value,   D_t = Q_t X + its local value.
 template <typename InT, typename OutT, bool CHAN, bool VEC>
-__global__ void __launch_bounds__(kSplitThreads, 2)
+__global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
     scan_backward_kernel(lq_scan_args a, lq_scan_grads g, const __grid_constant__ RowMap map_v,
                          const __grid_constant__ RowMap map_y, const __grid_constant__ RowMap map_g, int heads, int units,
                          int d, int lanes) {
     constexpr int R = backward_run(sizeof(InT) == 2, CHAN);
+    constexpr int NW = kBackwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Bars bars;
-    const int rows = kWorkers / lanes, chunk = rows * R;
-    const BackwardSpace<InT, OutT, CHAN> space(chunk, d);
+    const int rows = 32 * NW / lanes, chunk = rows * R;
+    const BackwardSpace<InT, OutT, CHAN> space(d, lanes, R);
     const int dp = space.dp, pitch = VEC ? d : dp;
-    const int y_at = chunk * pitch * (int)sizeof(InT), gates_at = y_at + chunk * pitch * (int)sizeof(OutT);
+    const int y_at = space.second(), gates_at = space.third();      // grad_out, and the log gates of channels, in a stage
     float *maps = reinterpret_cast<float *>(smem + kStages * space.stage());
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    if (tid == 0) init_bars(bars);
+    if (tid == 0) init_bars(bars, NW);
     __syncthreads();
     if (ranks > 1) cluster.sync();
 
@@ -689,72 +764,67 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const float *pg = a.g + row_of(a.g_stride, w, 0);
     const float *pb = a.beta != nullptr ? a.beta + row_of(a.beta_stride, w, 0) : nullptr;
 
-    if (warp == kWorkerWarps + 1) {                  // the loader
-        Turn turn;
+    if (warp == NW) {                                // the loader
         const int v_bytes = d * (int)sizeof(InT), y_bytes = py != nullptr ? d * (int)sizeof(OutT) : 0;
-        for (int s = 0; s < steps; ++s, turn.next()) {
-            const int t_cta = first_of(s), live = min(max(w.len - t_cta, 0), chunk);
-            if (s >= kStages && !mbar_wait(&bars.empty[turn.stage], turn.parity ^ 1, kWaitBudgetCycles)) break;
-            unsigned char *base = smem + turn.stage * space.stage();
-            float2 *sc = reinterpret_cast<float2 *>(base + space.scalars());
-            uint64_t *full = &bars.full[turn.stage];
+        auto live_of = [&](int s) { return min(max(w.len - first_of(s), 0), chunk); };
+        auto issue = [&](int s, int stage) {         // the copies of a step, one group of them
+            const int t_cta = first_of(s), live = live_of(s);
+            unsigned char *base = smem + stage * space.stage();
+            uint64_t *full = &bars.full[stage];
             if (lane == 0) {
-                mbar_arrive_expect_tx(full, VEC && live > 0 ? (uint32_t)(chunk * (v_bytes + y_bytes + (CHAN ? d * 4 : 0))) : 0u);
-                if (VEC && live > 0) {
+                const bool any = VEC && live > 0;
+                mbar_arrive_expect_tx(full, any ? (uint32_t)(chunk * (v_bytes + y_bytes + (CHAN ? d * 4 : 0))) : 0u);
+                if (any) {
                     bring_boxes(base, map_v, w, t_cta, chunk, v_bytes, full);
                     if (py != nullptr) bring_boxes(base + y_at, map_y, w, t_cta, chunk, y_bytes, full);
                     if (CHAN) bring_boxes(base + gates_at, map_g, w, t_cta, chunk, d * 4, full);
                 }
             }
-            for (int i = lane; i < live; i += 32) {
-                if (!CHAN) cp_async4(&sc[i].x, pg + (t_cta + i) * a.g_stride.token);
-                if (pb != nullptr) cp_async4(&sc[i].y, pb + (t_cta + i) * a.beta_stride.token);
+            float2 *sc = reinterpret_cast<float2 *>(base + space.scalars());
+            for (int j = lane; j < live; j += 32) {
+                if (!CHAN) cp_async4(&sc[j].x, pg + (t_cta + j) * a.g_stride.token);
+                if (pb != nullptr) cp_async4(&sc[j].y, pb + (t_cta + j) * a.beta_stride.token);
             }
-            cp_async_arrive(full);
-        }
-    } else if (warp == kWorkerWarps) {               // the composer
-        Composer<CHAN, true> composer{maps + 2 * space.map(), bars.peer, ranks, rank, dp};
-        const int64_t state = (int64_t)w.u * d;
-        float4 mark[2];              // the state before the CTA's tokens of the step
-        auto mark_of = [&](int s) {
-            for (int j = 0; j < 2; ++j) {
-                const int c = 4 * (lane + 32 * j), t_cta = first_of(s);
-                const bool live = s < steps && t_cta < w.len;
-                mark[j] = live ? load4(a.checkpoints + (int64_t)(t_cta / chunk) * units * d + state + c, d - c) : four(0.0f);
-            }
+            float *mark = reinterpret_cast<float *>(base + space.mark());
+            const float *from = a.checkpoints + ((int64_t)(t_cta / chunk) * units + w.u) * d;
+            if (live > 0)
+                for (int c = lane; c < d; c += 32) cp_async4(mark + c, from + c);
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        for (int j = 0; j < 2; ++j) {
-            const int c = 4 * (lane + 32 * j);
-            composer.carry[j] = g.grad_last != nullptr ? load4(g.grad_last + state + c, d - c) : four(0.0f);
-        }
-        mark_of(0);
-        for (int s = 0; s < steps; ++s) {
-            float *H = maps + (s & 1) * space.map(), *E = H + kWorkerWarps * dp, *A = E + kWorkerWarps * dp;
-            maps_barrier();
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (j >= composer.owned()) break;
-                const int q = lane + 32 * j;
-#pragma unroll
-                for (int k = 0; k < kWorkerWarps; ++k) {
-                    const Map4 m = composer.map(H, A, k, q);
-                    *reinterpret_cast<float4 *>(H + k * dp + 4 * q) = mark[j];
-                    mark[j] = apply(m, mark[j]);
+        // Once a step's copies have landed its gates are raised and it is
+        // announced, before the loader waits for the workers to leave a stage.
+        Turn now, next, left;
+        if (steps > 0) issue(0, 0);
+        if (steps > 1) issue(1, 1);
+        next.next();
+        for (int s = 0; s < steps; ++s, now.next()) {
+            if (s + 1 < steps) asm volatile("cp.async.wait_group 1;" ::: "memory");      // step s + 1 may be on its way
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            float2 *sc = reinterpret_cast<float2 *>(smem + now.stage * space.stage() + space.scalars());
+            for (int j = lane, live = live_of(s); j < live; j += 32) {                  // (the lane's own copies)
+                if (!CHAN) sc[j].x = gate_of(sc[j].x);
+                if (pb == nullptr) sc[j].y = 1.0f;
+            }
+            mbar_arrive(&bars.full[now.stage]);
+            next.next();
+            if (s + 2 < steps) {
+                if (s + 2 >= kStages) {
+                    if (!mbar_wait(&bars.empty[left.stage], left.parity, kWaitBudgetCycles)) break;
+                    left.next();
                 }
+                issue(s + 2, next.stage);
             }
-            mark_of(s + 1);
-            composer.run(s, E, A);
         }
-        maps_barrier();
-        if (rank == 0 && g.grad_h0 != nullptr)
-            for (int j = 0; j < 2; ++j) {
-                const int c = 4 * (lane + 32 * j);
-                store4(g.grad_h0 + state + c, d - c, composer.carry[j]);
-            }
     } else {                                         // the workers
-        const int c0 = (lane % lanes) * 8, row = tid / lanes;
+        const int in_row = lane & (lanes - 1), c0 = in_row * 8, row = tid / lanes;
         const bool on = c0 < d;
-        const int n = on ? min(8, d - c0) : 0;
+        const int n = on ? min(8, d - c0) : 0, cr = on ? c0 : 0;     // (lanes past d run with others' channels)
+        const int last_row = (tid | 31) / lanes;                     // of the warp
+        const int group = max(lanes, 16), in_group = lane & (group - 1), per_group = group / lanes;
+        const int first = row & ~(per_group - 1), last = first + per_group - 1;      // rows of the group
+        const int groups = 32 * NW / group, gate_row = space.gate_row(), peer = space.peer();
+        float *peers = maps + space.maps();
+        float *sH = maps, *sE = maps + space.E(), *sA = maps + space.A(), *sB = maps + space.B();
         auto bring = [&](int s, int stage) {
             if (!on || s >= steps) return;
             const int t_row = first_of(s) + row * R, live = min(max(w.len - t_row, 0), R);
@@ -766,191 +836,244 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         };
         if (!VEC)
             for (int s = 0; s < kStages; ++s) bring(s, s);
-        // eight channels of grad_out; channels past d are no part of any sum
-        auto grad_of = [&](const unsigned char *base, int i, float2 *y) {
+
+        // where the row's results go, step after step
+        constexpr int N = CHAN ? R : 2 * R;          // sums over a token's channels: grad_beta, then grad_g
+        const int t_start = first_of(0) + row * R;
+        InT *gv = static_cast<InT *>(g.grad_v) + row_of(g.grad_v_stride, w, t_start) + c0;
+        float *gg = g.grad_g + row_of(g.grad_g_stride, w, t_start) + c0;
+        const int sum_index = sum_of<N>(lanes, lane), sum_token = sum_index % R;     // the sum that this lane is left with
+        const bool is_beta = sum_index < R, writer = lanes >= N && (lane & (lanes / N - 1)) == 0;
+        const lq_strides &sum_stride = is_beta ? g.grad_beta_stride : g.grad_g_stride;
+        float *sum_at = is_beta ? g.grad_beta : g.grad_g;
+        const bool puts = writer && sum_at != nullptr;
+        sum_at += row_of(sum_stride, w, t_start + sum_token);
+        const int64_t gv_step = stride * g.grad_v_stride.token, gg_step = stride * g.grad_g_stride.token,
+                      sum_step = stride * sum_stride.token;
+
+        // what enters a step from behind, of channels tid and tid + 32 NW
+        float carry[2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = make_float2(0.0f, 0.0f);
-            if (py != nullptr) read_shared<OutT>(base + y_at, pitch, row * R + i, c0, y);
-        };
+        for (int j = 0; j < 2; ++j) {
+            const int c = tid + 32 * NW * j;
+            carry[j] = c < d && g.grad_last != nullptr ? g.grad_last[(int64_t)w.u * d + c] : 0.0f;
+        }
         bool alive = true;           // a wait that ran out is the last one, and what follows it is NaN
-        Turn one, two;               // the stages of pass one and pass two
-        Gates<CHAN> A_before, B_after;           // of the step whose pass two is due: the maps of its warp's rows
-        float2 H_before[4], E_after[4];          // before and after this one
-        for (int s = 0; s <= steps; ++s) {
-            Gates<CHAN> A, B;
-            float2 H[4] = {}, E[4] = {};
+        Turn turn;
+        for (int s = 0; s < steps; ++s) {
+            const int t_row = first_of(s) + row * R, live = min(max(w.len - t_row, 0), R);
+            const bool full_rows = first_of(s) + (last_row + 1) * R <= w.len;        // every row of the warp has R tokens
+            const unsigned char *base = smem + turn.stage * space.stage();
+            const float2 *sc = reinterpret_cast<const float2 *>(base + space.scalars()) + row * R;
+            Gates<CHAN> P[R], Q[R], A, B;
+            float2 ah[R][4], D[R][4], H[4] = {}, E[4] = {};
             A.fill(1.0f);
-            if (s < steps) {
-                const int live = min(max(w.len - (first_of(s) + row * R), 0), R);
-                unsigned char *base = smem + one.stage * space.stage();
-                float2 *sc = reinterpret_cast<float2 *>(base + space.scalars()) + row * R;
-                float *sH = maps + (s & 1) * space.map(), *sE = sH + kWorkerWarps * dp, *sA = sE + kWorkerWarps * dp;
-                if (alive) alive = mbar_wait(&bars.full[one.stage], one.parity, kWaitBudgetCycles);
-                if (!alive) A.fill(nanf(""));
-                if (!CHAN) {                         // each gate is raised once, by one lane of its row
-                    for (int i = lane % lanes; i < live; i += lanes) sc[i].x = gate_of(sc[i].x);
-                    __syncwarp();
-                }
+            B.fill(1.0f);
+            if (alive) alive = mbar_wait(&bars.full[turn.stage], turn.parity, kWaitBudgetCycles);
+            if (!alive) A.fill(nanf(""));
+            auto pass = [&](auto FULL) {             // FULL: a straight line of code
                 Gates<CHAN> gate[R];
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
+                    float beta = 0.0f;
+                    float2 v[4] = {};
                     gate[i].fill(1.0f);
-                    if (i < live && on) {
+                    if (FULL || (i < live && on)) {
                         const float2 gb = sc[i];
-                        const float b = pb != nullptr ? gb.y : 1.0f;
-                        if constexpr (CHAN) {        // raised once: pass two finds alpha in its place
-                            float *q = reinterpret_cast<float *>(base + gates_at) + (row * R + i) * pitch + c0;
-                            read_shared(q, gate[i].a);
+                        beta = gb.y;
+                        if constexpr (CHAN) {
+                            read_shared<float>(base + gates_at, pitch, row * R + i, cr, gate[i].a);
                             gate[i].exponentiate();
-                            store8<true>(q, n, gate[i].a);
                         } else {
                             gate[i].fill(gb.x);
                         }
-                        float2 v[4];
-                        read_shared<InT>(base, pitch, row * R + i, c0, v);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) H[c] = fma2(gate[i][c], H[c], mul2(make_float2(b, b), v[c]));
-                        A.times(gate[i]);
+                        read_shared<InT>(base, pitch, row * R + i, cr, v);
                     }
-                }
-#pragma unroll
-                for (int i = R - 1; i >= 0; --i) {
-                    if (i < live && on) {
-                        float2 y[4];
-                        grad_of(base, i, y);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) E[c] = mul2(gate[i][c], add2(y[c], E[c]));
-                    }
-                }
-                B = A;
-                for (int o = lanes; o < 32; o *= 2) {
-                    const Gates<CHAN> ap = A.before(o), bp = B.after(o);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float2 hp = pair_before(H[c], o), ep = pair_after(E[c], o);
-                        if (lane >= o) H[c] = fma2(A[c], hp, H[c]);
-                        if (lane + o < 32) E[c] = fma2(B[c], ep, E[c]);
+                        ah[i][c] = mul2(gate[i][c], H[c]);
+                        H[c] = fma2(make_float2(beta, beta), v[c], ah[i][c]);
                     }
-                    if (lane >= o) A.times(ap);
-                    if (lane + o < 32) B.times(bp);
+                    A.times(gate[i]);
+                    P[i] = A;
                 }
-                if (on && lane >= 32 - lanes) {
-                    store8<true>(sH + warp * dp + c0, 8, H);
-                    if constexpr (CHAN) store8<true>(sA + warp * dp + c0, 8, A.a);
-                    else if (c0 == 0) *reinterpret_cast<float4 *>(sA + warp * 4) = four(A.a[0].x);
-                }
-                if (on && lane < lanes) store8<true>(sE + warp * dp + c0, 8, E);
-                A = A.before(lanes);
-                B = B.after(lanes);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    H[c] = pair_before(H[c], lanes);
-                    E[c] = pair_after(E[c], lanes);
-                }
-                one.next();
-            }
-            maps_barrier();          // the maps of step s are there, and what enters the warps of step s - 1
-            if (s > 0) {
-                const int t_row = first_of(s - 1) + row * R, live = min(max(w.len - t_row, 0), R);
-                const unsigned char *base = smem + two.stage * space.stage();
-                const float2 *sc = reinterpret_cast<const float2 *>(base + space.scalars()) + row * R;
-                const float *sH = maps + ((s - 1) & 1) * space.map(), *sE = sH + kWorkerWarps * dp;
-                float2 h[4] = {}, x[4] = {}, ah[R][4];           // ah = alpha_t h_{t-1}
-                if (on) {
-                    read_shared(sH + warp * dp + c0, h);
-                    read_shared(sE + warp * dp + c0, x);
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (lane >= lanes) h[c] = fma2(A_before[c], h[c], H_before[c]);
-                    if (lane + lanes < 32) x[c] = fma2(B_after[c], x[c], E_after[c]);
-                }
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    if (i < live && on) {
-                        const float2 gb = sc[i];
-                        const float b = pb != nullptr ? gb.y : 1.0f;
-                        Gates<CHAN> gate;
-                        if constexpr (CHAN) read_shared<float>(base + gates_at, pitch, row * R + i, c0, gate.a);
-                        else gate.fill(gb.x);
-                        float2 v[4];
-                        read_shared<InT>(base, pitch, row * R + i, c0, v);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            ah[i][c] = mul2(gate[c], h[c]);
-                            h[c] = fma2(make_float2(b, b), v[c], ah[i][c]);
-                        }
-                    }
-                }
-                constexpr int N = CHAN ? R : 2 * R;              // sums over a token's channels: grad_beta, then grad_g
-                float sums[N] = {};
-                InT *gv = static_cast<InT *>(g.grad_v) + row_of(g.grad_v_stride, w, t_row) + c0;
-                float *gg = g.grad_g + row_of(g.grad_g_stride, w, t_row) + (CHAN ? c0 : 0);
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
-                    if (i < live && on) {
-                        const float2 gb = sc[i];
-                        const float b = pb != nullptr ? gb.y : 1.0f;
-                        Gates<CHAN> gate;
-                        if constexpr (CHAN) read_shared<float>(base + gates_at, pitch, row * R + i, c0, gate.a);
-                        else gate.fill(gb.x);
-                        float2 y[4], v[4], dv[4], sb = {}, sg = {};
-                        grad_of(base, i, y);
-                        read_shared<InT>(base, pitch, row * R + i, c0, v);
+                    float2 y[4] = {};
+                    if ((FULL || (i < live && on)) && py != nullptr) read_shared<OutT>(base + y_at, pitch, row * R + i, cr, y);
+                    Q[i] = B;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float2 D = add2(y[c], x[c]);
-                            x[c] = mul2(gate[c], D);
-                            dv[c] = mul2(make_float2(b, b), D);
-                            y[c] = mul2(ah[i][c], D);            // grad_g of the channel
-                            if (2 * c < n) {                     // (beyond an odd d the pair's second half is zero)
-                                sb = fma2(v[c], D, sb);
-                                sg = add2(sg, y[c]);
-                            }
-                        }
-                        sums[i] = sb.x + sb.y;
-                        if (!CHAN) sums[N - R + i] = sg.x + sg.y;
-                        if (g.grad_v != nullptr) store8<VEC>(gv + i * g.grad_v_stride.token, n, dv);
-                        if (CHAN && g.grad_g != nullptr) store8<VEC>(gg + i * g.grad_g_stride.token, n, y);
+                    for (int c = 0; c < 4; ++c) {
+                        D[i][c] = add2(y[c], E[c]);
+                        E[c] = mul2(gate[i][c], D[i][c]);
+                    }
+                    B.times(gate[i]);
+                }
+            };
+            if (full_rows) pass(std::true_type());
+            else pass(std::false_type());
+            for (int o = lanes; o < group; o *= 2) {
+                const Gates<CHAN> ap = A.before(o), bp = B.after(o);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 hp = pair_before(H[c], o), ep = pair_after(E[c], o);
+                    if (in_group >= o) H[c] = fma2(A[c], hp, H[c]);
+                    if (in_group + o < group) E[c] = fma2(B[c], ep, E[c]);
+                }
+                if (in_group >= o) A.times(ap);
+                if (in_group + o < group) B.times(bp);
+            }
+            if (on) {
+                store8<true>(sH + row * dp + c0, 8, H);
+                store8<true>(sE + row * dp + c0, 8, E);
+                if constexpr (CHAN) {
+                    store8<true>(sA + row * dp + c0, 8, A.a);
+                    if (per_group > 1) store8<true>(sB + row * dp + c0, 8, B.a);
+                } else if (c0 == 0) {
+                    sA[row] = A.a;
+                    sB[row] = B.a;
+                }
+            }
+            meet<1, 32 * NW>();
+            // A thread composes one channel: the groups' H and E are replaced by
+            // what enters them.  A group's H and A are its last row's, its E its
+            // first row's.  The cluster's maps cross as Composer's do.
+            const int step_h = per_group * dp, step_a = per_group * gate_row, p = s & 1;
+            if (ranks > 1) {         // this CTA's map to the cluster
+                if (tid == 0) mbar_arrive_expect_tx(bars.peer + p, (uint32_t)(ranks * (CHAN ? 2 * dp : dp + 1) * 4));
+                const uint32_t at = smem_u32(peers + (p * ranks + rank) * peer), bar = smem_u32(bars.peer + p);
+                for (int c = tid; c < dp; c += 32 * NW) {
+                    const float *Ec = sE + c, *Ac = sA + (per_group - 1) * gate_row + (CHAN ? c : 0);
+                    float all_a = 1.0f, all_e = 0.0f;
+                    for (int k = groups - 1; k >= 0; --k) {
+                        all_e = fmaf(Ac[k * step_a], all_e, Ec[k * step_h]);
+                        all_a *= Ac[k * step_a];
+                    }
+                    for (int r = 0; r < ranks; ++r) {
+                        const uint32_t dst = peer_address(at, r), b = peer_address(bar, r);
+                        peer_store(dst + c * 4, all_e, b);
+                        if (CHAN || c == 0) peer_store(dst + (dp + c) * 4, all_a, b);
                     }
                 }
-                float *gb_row = g.grad_beta != nullptr ? g.grad_beta + row_of(g.grad_beta_stride, w, t_row) : nullptr;
-                if (!CHAN || gb_row != nullptr) {
-                    auto put = [&](int j, float x) {
-                        const int i = j % R;
-                        if (i >= live) return;
-                        if (j < R) {
-                            if (gb_row != nullptr) gb_row[i * g.grad_beta_stride.token] = x;
-                        } else if (g.grad_g != nullptr) {
-                            gg[i * g.grad_g_stride.token] = x;
-                        }
-                    };
-                    if (lanes >= N) {
-                        int j;
-                        const float x = sum_row(sums, lanes, lane, &j);
-                        if (lane % (lanes / N) == 0) put(j, x);
-                    } else {
+            }
 #pragma unroll
-                        for (int j = 0; j < N; ++j) {
-                            for (int o = lanes / 2; o >= 1; o /= 2) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
-                            if (c0 == 0) put(j, sums[j]);
+            for (int j = 0; j < 2; ++j) {
+                const int c = tid + 32 * NW * j;
+                if (c >= dp) break;
+                float *Hc = sH + (per_group - 1) * dp + c, *Ec = sE + c;
+                const float *Ac = sA + (per_group - 1) * gate_row + (CHAN ? c : 0);
+                float h = c < d ? reinterpret_cast<const float *>(base + space.mark())[c] : 0.0f;
+                static_assert(NW % 3 == 0, "groups of rows in threes");
+                for (int k = 0; k < groups; k += 3) {            // (three are read before one is replaced)
+                    const float h0 = Hc[k * step_h], h1 = Hc[(k + 1) * step_h], h2 = Hc[(k + 2) * step_h];
+                    const float a0 = Ac[k * step_a], a1 = Ac[(k + 1) * step_a], a2 = Ac[(k + 2) * step_a];
+                    Hc[k * step_h] = h;
+                    h = fmaf(a0, h, h0);
+                    Hc[(k + 1) * step_h] = h;
+                    h = fmaf(a1, h, h1);
+                    Hc[(k + 2) * step_h] = h;
+                    h = fmaf(a2, h, h2);
+                }
+                float x = carry[j];
+                if (ranks > 1) {
+                    if (alive) alive = peer_wait(bars.peer + p, (s >> 1) & 1);
+                    if (!alive) carry[j] = nanf("");
+                    for (int r = ranks - 1; r >= 0; --r) {
+                        const float *m = peers + (p * ranks + r) * peer;
+                        if (r == rank) x = carry[j];
+                        carry[j] = fmaf(m[dp + (CHAN ? c : 0)], carry[j], m[c]);
+                    }
+                }
+                for (int k = groups - 1; k >= 0; k -= 3) {
+                    const float e0 = Ec[k * step_h], e1 = Ec[(k - 1) * step_h], e2 = Ec[(k - 2) * step_h];
+                    const float a0 = Ac[k * step_a], a1 = Ac[(k - 1) * step_a], a2 = Ac[(k - 2) * step_a];
+                    Ec[k * step_h] = x;
+                    x = fmaf(a0, x, e0);
+                    Ec[(k - 1) * step_h] = x;
+                    x = fmaf(a1, x, e1);
+                    Ec[(k - 2) * step_h] = x;
+                    x = fmaf(a2, x, e2);
+                }
+                if (ranks == 1) carry[j] = x;
+            }
+            meet<1, 32 * NW>();      // what enters the groups of rows is there
+            float2 h[4], x[4];
+            read_shared(sH + last * dp + cr, h);
+            read_shared(sE + first * dp + cr, x);
+            if (per_group > 1) {     // the maps of the group's rows before and after this one
+                if (row != first) {
+                    Gates<CHAN> m;
+                    float2 y[4];
+                    if constexpr (CHAN) read_shared(sA + (row - 1) * dp + cr, m.a);
+                    else m.fill(sA[row - 1]);
+                    read_shared(sH + (row - 1) * dp + cr, y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) h[c] = fma2(m[c], h[c], y[c]);
+                }
+                if (row != last) {
+                    Gates<CHAN> m;
+                    float2 y[4];
+                    if constexpr (CHAN) read_shared(sB + (row + 1) * dp + cr, m.a);
+                    else m.fill(sB[row + 1]);
+                    read_shared(sE + (row + 1) * dp + cr, y);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[c] = fma2(m[c], x[c], y[c]);
+                }
+                __syncwarp();        // the group's rows have read each other's maps
+            }
+            float sums[N];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float2 v[4], dv[4], dg[4], sb = {}, sg = {};
+                read_shared<InT>(base, pitch, row * R + i, cr, v);
+                const float beta = sc[i].y;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 Dt = fma2(Q[i][c], x[c], D[i][c]), aht = fma2(P[i][c], h[c], ah[i][c]);
+                    dv[c] = mul2(make_float2(beta, beta), Dt);
+                    if (CHAN) dg[c] = mul2(aht, Dt);
+                    if (2 * c < n) {                 // (beyond an odd d the pair's second half is zero)
+                        sb = fma2(v[c], Dt, sb);
+                        if (!CHAN) sg = fma2(aht, Dt, sg);
+                    }
+                }
+                sums[i] = sb.x + sb.y;
+                if (!CHAN) sums[N - R + i] = sg.x + sg.y;
+                if (on && i < live) {
+                    if (g.grad_v != nullptr) store8<VEC>(gv + i * g.grad_v_stride.token, n, dv);
+                    if (CHAN && g.grad_g != nullptr) store8<VEC>(gg + i * g.grad_g_stride.token, n, dg);
+                }
+            }
+            if (!CHAN || g.grad_beta != nullptr) {
+                if (lanes >= N) {
+                    const float sum = sum_row(sums, lanes, lane);
+                    if (puts && sum_token < live) *sum_at = sum;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        for (int o = lanes / 2; o >= 1; o /= 2) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
+                        const int t = t_row + j % R;
+                        if (c0 == 0 && j % R < live) {
+                            if (j < R && g.grad_beta != nullptr) g.grad_beta[row_of(g.grad_beta_stride, w, t)] = sums[j];
+                            if (j >= R && g.grad_g != nullptr) g.grad_g[row_of(g.grad_g_stride, w, t)] = sums[j];
                         }
                     }
                 }
-                if (!VEC) bring(s - 1 + kStages, two.stage);
-                if (CHAN) fence_proxy_async_smem();  // alpha was written where the next copy lands
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.empty[two.stage]);
-                two.next();
             }
-            A_before = A;
-            B_after = B;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                H_before[c] = H[c];
-                E_after[c] = E[c];
-            }
+            gv -= gv_step;
+            gg -= gg_step;
+            sum_at -= sum_step;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.empty[turn.stage]);     // the stage is read
+            if (!VEC) bring(s + kStages, turn.stage);
+            turn.next();
         }
+        if (rank == 0 && g.grad_h0 != nullptr)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = tid + 32 * NW * j;
+                if (c < d) g.grad_h0[(int64_t)w.u * d + c] = carry[j];
+            }
         if (a.zero_past && on) {
             const float2 zero[4] = {};
             for (int t = w.len + rank * rows + row; t < a.n_tokens; t += ranks * rows) {
@@ -993,12 +1116,12 @@ cudaError_t by_variant(const lq_scan_config &c, bool vec, F &&f) {
 // A launch of `ranks` CTAs a unit as clusters.  `most`: the dynamic shared
 // memory that the kernel may ask for at all.
 template <auto kernel, typename... V>
-cudaError_t launch_clusters(int units, int ranks, int smem, int most, cudaStream_t s, const V &...args) {
+cudaError_t launch_clusters(int threads, int units, int ranks, int smem, int most, cudaStream_t s, const V &...args) {
     const cudaError_t e = opt_in_smem<kernel>(most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)units * (unsigned)ranks);
-    cfg.blockDim = dim3(kSplitThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute at;
@@ -1022,7 +1145,7 @@ cudaError_t row_map(RowMap *m, const void *p, const lq_strides &s, const lq_scan
     const cuuint64_t strides[3] = {c.heads > 1 ? (cuuint64_t)s.head * size : row,
                                    c.batch > 1 ? (cuuint64_t)s.seq * size : row,
                                    tokens > 1 ? (cuuint64_t)s.token * size : row};
-    const cuuint32_t box[4] = {(cuuint32_t)c.d, 1, 1, (cuuint32_t)std::min(chunk, kMostBox)};
+    const cuuint32_t box[4] = {(cuuint32_t)c.d, 1, 1, (cuuint32_t)box_of(chunk)};
     const cuuint32_t each[4] = {1, 1, 1, 1};
     const CUresult r = encode(&m->map, dtype == LQ_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                               4, const_cast<void *>(p), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1031,36 +1154,33 @@ cudaError_t row_map(RowMap *m, const void *p, const lq_strides &s, const lq_scan
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// CTAs that share a unit: the number that takes the fewest steps one after
-// another, counting two steps' time for the start and end of each round of CTAs
-// on the device.
-int ranks_of(int units, long long tokens, int chunk, int ctas_per_sm) {
-    const long long slots = (long long)ctas_per_sm * sm_count();
-    int best = 1;
+// How a call is split: the CTAs that share a unit, a CTA's shared memory, and
+// the most that any d wants (for the kernel's limit).
+struct Plan {
+    int ranks, smem, most, chunk;
+};
+
+// As many CTAs as take the fewest steps one after another, counting two steps'
+// time for the start and end of each round of CTAs on the device.  Registers
+// leave two CTAs to an SM, and shared memory one or two.
+template <typename S>
+Plan plan_of(int units, long long tokens, int d, int run) {
+    auto space = [run](int dd) { return S(dd, row_lanes(dd), run); };
+    Plan p{1, 0, 0, space(d).tokens};
     long long least = -1;
     for (int r = 1; r <= kMostRanks; ++r) {
-        const long long rounds = ((long long)units * r + slots - 1) / slots, stride = (long long)r * chunk;
+        const int smem = space(d).bytes(r);
+        const long long slots = (2 * (smem + 2048) <= 228 * 1024 ? 2 : 1) * (long long)sm_count();
+        const long long rounds = ((long long)units * r + slots - 1) / slots, stride = (long long)r * p.chunk;
         const long long cost = rounds * ((tokens + stride - 1) / stride + 2);
         if (least < 0 || cost < least) {
             least = cost;
-            best = r;
+            p.ranks = r;
+            p.smem = smem;
         }
     }
-    return best;
-}
-
-// Shared memory of a kernel whose stages are S: what a call needs, the most
-// that any d wants, and the CTAs that then fit an SM (registers leave two).
-struct Room {
-    int smem, most, ctas;
-};
-template <typename S>
-Room room_of(int d, int run) {
-    auto bytes = [run](int dd) { return S(kWorkers / row_lanes(dd) * run, dd).bytes(kMostRanks); };
-    Room r{bytes(d), 0, 1};
-    for (int dd = 8; dd <= 256; dd *= 2) r.most = std::max(r.most, bytes(dd));
-    if (2 * (r.smem + 2048) <= 228 * 1024) r.ctas = 2;
-    return r;
+    for (int dd = 8; dd <= 256; dd *= 2) p.most = std::max(p.most, space(dd).bytes(kMostRanks));
+    return p;
 }
 
 }  // namespace
@@ -1078,16 +1198,15 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
             return cudaGetLastError();
         }
         constexpr int run = forward_run(sizeof(In) == 2, K::CHAN);
-        const Room room = room_of<ForwardSpace<In, K::CHAN>>(c.d, run);
-        const int chunk = kWorkers / lanes * run, ranks = ranks_of(units, a.n_tokens, chunk, room.ctas);
+        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run);
         RowMap v = {}, g = {};
         if (K::VEC) {
-            cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, chunk);
-            if (e == cudaSuccess && K::CHAN) e = row_map(&g, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, chunk);
+            cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
+            if (e == cudaSuccess && K::CHAN) e = row_map(&g, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
         return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC>>(
-            units, ranks, room.smem, room.most, s, a, v, g, c.heads, units, c.d, lanes, every);
+            32 * kForwardWarps + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, lanes, every);
     });
 }
 
@@ -1099,18 +1218,17 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
         using In = typename K::In;
         using Out = typename K::Out;
         constexpr int run = backward_run(sizeof(In) == 2, K::CHAN);
-        const Room room = room_of<BackwardSpace<In, Out, K::CHAN>>(c.d, run);
-        const int chunk = kWorkers / lanes * run, ranks = ranks_of(units, a.n_tokens, chunk, room.ctas);
+        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run);
         RowMap v = {}, y = {}, gate = {};
         if (K::VEC) {
-            cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, chunk);
+            cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
             if (e == cudaSuccess && g.grad_out != nullptr)
-                e = row_map(&y, g.grad_out, g.grad_out_stride, c, a.n_tokens, c.out_dtype, chunk);
-            if (e == cudaSuccess && K::CHAN) e = row_map(&gate, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, chunk);
+                e = row_map(&y, g.grad_out, g.grad_out_stride, c, a.n_tokens, c.out_dtype, p.chunk);
+            if (e == cudaSuccess && K::CHAN) e = row_map(&gate, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
         return launch_clusters<scan_backward_kernel<In, Out, K::CHAN, K::VEC>>(
-            units, ranks, room.smem, room.most, s, a, g, v, y, gate, c.heads, units, c.d, lanes);
+            32 * kBackwardWarps + 32, units, p.ranks, p.smem, p.most, s, a, g, v, y, gate, c.heads, units, c.d, lanes);
     });
 }
 
