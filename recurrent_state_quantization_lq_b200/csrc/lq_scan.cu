@@ -489,10 +489,11 @@ __global__ void __launch_bounds__(kRowsThreads) scan_rows_kernel(lq_scan_args a,
 template <typename InT, bool CHAN>
 using ForwardSpace = Space<kForwardWarps, (int)sizeof(InT), CHAN ? 4 : 0, 0, CHAN, false>;
 
-template <typename InT, typename OutT, bool CHAN, bool VEC>
+template <typename InT, typename OutT, bool CHAN, bool VEC, int LANES>
 __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
     scan_forward_kernel(lq_scan_args a, const __grid_constant__ RowMap map_v, const __grid_constant__ RowMap map_g,
-                        int heads, int units, int d, int lanes, int every) {
+                        int heads, int units, int d, int any_lanes, int every) {
+    const int lanes = LANES > 0 ? LANES : any_lanes;
     constexpr int R = forward_run(sizeof(InT) == 2, CHAN);
     constexpr int NW = kForwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -735,11 +736,12 @@ using BackwardSpace = Space<kBackwardWarps, (int)sizeof(InT), (int)sizeof(OutT),
 // cluster.  With h what enters the row from before and X from behind, P_t the
 // product of its gates up to t and Q_t of those after t, pass two has
 //     alpha_t h_{t-1} = P_t h + its local value,   D_t = Q_t X + its local value.
-template <typename InT, typename OutT, bool CHAN, bool VEC>
-__global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
+template <typename InT, typename OutT, bool CHAN, bool VEC, int LANES>
+__global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
     scan_backward_kernel(lq_scan_args a, lq_scan_grads g, const __grid_constant__ RowMap map_v,
                          const __grid_constant__ RowMap map_y, const __grid_constant__ RowMap map_g, int heads, int units,
-                         int d, int lanes) {
+                         int d, int any_lanes) {
+    const int lanes = LANES > 0 ? LANES : any_lanes;
     constexpr int R = backward_run(sizeof(InT) == 2, CHAN);
     constexpr int NW = kBackwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -820,7 +822,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
         const bool on = c0 < d;
         const int n = on ? min(8, d - c0) : 0, cr = on ? c0 : 0;     // (lanes past d run with others' channels)
         const int last_row = (tid | 31) / lanes;                     // of the warp
-        const int group = max(lanes, 16), in_group = lane & (group - 1), per_group = group / lanes;
+        const int group = max(lanes, 8), in_group = lane & (group - 1), per_group = group / lanes;
         const int first = row & ~(per_group - 1), last = first + per_group - 1;      // rows of the group
         const int groups = 32 * NW / group, gate_row = space.gate_row(), peer = space.peer();
         float *peers = maps + space.maps();
@@ -851,12 +853,16 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
         const int64_t gv_step = stride * g.grad_v_stride.token, gg_step = stride * g.grad_g_stride.token,
                       sum_step = stride * sum_stride.token;
 
-        // what enters a step from behind, of channels tid and tid + 32 NW
-        float carry[2];
+        // A thread composes channel tid (and tid + 32 NW where there are as many);
+        // where half of the threads are enough for the states, the other half
+        // composes the gradients.
+        constexpr int NC = LANES > 0 && LANES <= 16 ? 1 : 2;
+        const int e_from = (LANES == 8 || (LANES == 0 && dp <= 16 * NW)) ? 16 * NW : 0;
+        float carry[NC];             // what enters a step from behind
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int c = tid + 32 * NW * j;
-            carry[j] = c < d && g.grad_last != nullptr ? g.grad_last[(int64_t)w.u * d + c] : 0.0f;
+        for (int j = 0; j < NC; ++j) {
+            const int c = tid - e_from + 32 * NW * j;
+            carry[j] = c >= 0 && c < d && g.grad_last != nullptr ? g.grad_last[(int64_t)w.u * d + c] : 0.0f;
         }
         bool alive = true;           // a wait that ran out is the last one, and what follows it is NaN
         Turn turn;
@@ -935,20 +941,29 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
                 }
             }
             meet<1, 32 * NW>();
-            // A thread composes one channel: the groups' H and E are replaced by
-            // what enters them.  A group's H and A are its last row's, its E its
-            // first row's.  The cluster's maps cross as Composer's do.
+            // The groups' H and E are replaced by what enters them.  A group's H and
+            // A are its last row's, its E its first row's.  The cluster's maps cross
+            // as Composer's do.
             const int step_h = per_group * dp, step_a = per_group * gate_row, p = s & 1;
+            const float *A_last = sA + (per_group - 1) * gate_row;
+            static_assert(NW % 3 == 0, "groups of rows in threes");
             if (ranks > 1) {         // this CTA's map to the cluster
-                if (tid == 0) mbar_arrive_expect_tx(bars.peer + p, (uint32_t)(ranks * (CHAN ? 2 * dp : dp + 1) * 4));
+                if (tid == e_from) mbar_arrive_expect_tx(bars.peer + p, (uint32_t)(ranks * (CHAN ? 2 * dp : dp + 1) * 4));
                 const uint32_t at = smem_u32(peers + (p * ranks + rank) * peer), bar = smem_u32(bars.peer + p);
-                for (int c = tid; c < dp; c += 32 * NW) {
-                    const float *Ec = sE + c, *Ac = sA + (per_group - 1) * gate_row + (CHAN ? c : 0);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    const int c = tid - e_from + 32 * NW * j;
+                    if (c < 0 || c >= dp) break;
+                    const float *Ec = sE + c, *Ac = A_last + (CHAN ? c : 0);
                     float all_a = 1.0f, all_e = 0.0f;
-                    for (int k = groups - 1; k >= 0; --k) {
-                        all_e = fmaf(Ac[k * step_a], all_e, Ec[k * step_h]);
-                        all_a *= Ac[k * step_a];
+#pragma unroll 1
+                    for (int k = groups - 1; k >= 0; k -= 3) {
+                        const float e0 = Ec[k * step_h], e1 = Ec[(k - 1) * step_h], e2 = Ec[(k - 2) * step_h];
+                        const float a0 = Ac[k * step_a], a1 = Ac[(k - 1) * step_a], a2 = Ac[(k - 2) * step_a];
+                        all_e = fmaf(a2, fmaf(a1, fmaf(a0, all_e, e0), e1), e2);
+                        all_a *= a0 * a1 * a2;
                     }
+#pragma unroll 1
                     for (int r = 0; r < ranks; ++r) {
                         const uint32_t dst = peer_address(at, r), b = peer_address(bar, r);
                         peer_store(dst + c * 4, all_e, b);
@@ -957,13 +972,13 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < NC; ++j) {           // the states, from the CTA's checkpoint on
                 const int c = tid + 32 * NW * j;
                 if (c >= dp) break;
-                float *Hc = sH + (per_group - 1) * dp + c, *Ec = sE + c;
-                const float *Ac = sA + (per_group - 1) * gate_row + (CHAN ? c : 0);
+                float *Hc = sH + (per_group - 1) * dp + c;
+                const float *Ac = A_last + (CHAN ? c : 0);
                 float h = c < d ? reinterpret_cast<const float *>(base + space.mark())[c] : 0.0f;
-                static_assert(NW % 3 == 0, "groups of rows in threes");
+#pragma unroll 1
                 for (int k = 0; k < groups; k += 3) {            // (three are read before one is replaced)
                     const float h0 = Hc[k * step_h], h1 = Hc[(k + 1) * step_h], h2 = Hc[(k + 2) * step_h];
                     const float a0 = Ac[k * step_a], a1 = Ac[(k + 1) * step_a], a2 = Ac[(k + 2) * step_a];
@@ -974,16 +989,25 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
                     Hc[(k + 2) * step_h] = h;
                     h = fmaf(a2, h, h2);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {           // the gradients
+                const int c = tid - e_from + 32 * NW * j;
+                if (c < 0 || c >= dp) break;
+                float *Ec = sE + c;
+                const float *Ac = A_last + (CHAN ? c : 0);
                 float x = carry[j];
                 if (ranks > 1) {
                     if (alive) alive = peer_wait(bars.peer + p, (s >> 1) & 1);
                     if (!alive) carry[j] = nanf("");
+#pragma unroll 1
                     for (int r = ranks - 1; r >= 0; --r) {
                         const float *m = peers + (p * ranks + r) * peer;
                         if (r == rank) x = carry[j];
                         carry[j] = fmaf(m[dp + (CHAN ? c : 0)], carry[j], m[c]);
                     }
                 }
+#pragma unroll 1
                 for (int k = groups - 1; k >= 0; k -= 3) {
                     const float e0 = Ec[k * step_h], e1 = Ec[(k - 1) * step_h], e2 = Ec[(k - 2) * step_h];
                     const float a0 = Ac[k * step_a], a1 = Ac[(k - 1) * step_a], a2 = Ac[(k - 2) * step_a];
@@ -1070,9 +1094,9 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
         }
         if (rank == 0 && g.grad_h0 != nullptr)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = tid + 32 * NW * j;
-                if (c < d) g.grad_h0[(int64_t)w.u * d + c] = carry[j];
+            for (int j = 0; j < NC; ++j) {
+                const int c = tid - e_from + 32 * NW * j;
+                if (c >= 0 && c < d) g.grad_h0[(int64_t)w.u * d + c] = carry[j];
             }
         if (a.zero_past && on) {
             const float2 zero[4] = {};
@@ -1091,17 +1115,35 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, 2)
 // ------------------------------------------------------------------ dispatch
 
 // A kernel's types and variants, as one value.
-template <typename In_, typename Out_, bool CHAN_, bool VEC_>
+template <typename In_, typename Out_, bool CHAN_, bool VEC_, int LANES_>
 struct Variant {
     using In = In_;
     using Out = Out_;
     static constexpr bool CHAN = CHAN_, VEC = VEC_;
+    static constexpr int LANES = LANES_;     // lanes of a row, where the kernel is compiled for them (0: any)
 };
+
+// Rows of 16-byte pieces, one type in and out, are compiled for the lanes of
+// heads of 33..64, 65..128 and 129..256 channels: known strides save a dozen
+// registers, and a spilled one costs thousands of cycles a step here.
+template <typename In, typename Out, bool CHAN, typename F>
+cudaError_t by_rows(const lq_scan_config &c, bool vec, F &&f) {
+    if constexpr (std::is_same<In, Out>::value) {
+        if (vec) {
+            switch (row_lanes(c.d)) {
+                case 8: return f(Variant<In, Out, CHAN, true, 8>());
+                case 16: return f(Variant<In, Out, CHAN, true, 16>());
+                case 32: return f(Variant<In, Out, CHAN, true, 32>());
+                default: break;
+            }
+        }
+    }
+    return vec ? f(Variant<In, Out, CHAN, true, 0>()) : f(Variant<In, Out, CHAN, false, 0>());
+}
 
 template <typename In, typename Out, typename F>
 cudaError_t by_gate(const lq_scan_config &c, bool vec, F &&f) {
-    if (c.gate == LQ_GATE_CHANNEL) return vec ? f(Variant<In, Out, true, true>()) : f(Variant<In, Out, true, false>());
-    return vec ? f(Variant<In, Out, false, true>()) : f(Variant<In, Out, false, false>());
+    return c.gate == LQ_GATE_CHANNEL ? by_rows<In, Out, true>(c, vec, f) : by_rows<In, Out, false>(c, vec, f);
 }
 
 template <typename F>
@@ -1111,7 +1153,6 @@ cudaError_t by_variant(const lq_scan_config &c, bool vec, F &&f) {
     if (c.in_dtype == LQ_DTYPE_BF16) return out_b ? by_gate<B, B>(c, vec, f) : by_gate<B, float>(c, vec, f);
     return out_b ? by_gate<float, B>(c, vec, f) : by_gate<float, float>(c, vec, f);
 }
-
 
 // A launch of `ranks` CTAs a unit as clusters.  `most`: the dynamic shared
 // memory that the kernel may ask for at all.
@@ -1162,15 +1203,15 @@ struct Plan {
 
 // As many CTAs as take the fewest steps one after another, counting two steps'
 // time for the start and end of each round of CTAs on the device.  Registers
-// leave two CTAs to an SM, and shared memory one or two.
+// leave most_ctas CTAs to an SM, and shared memory one or two.
 template <typename S>
-Plan plan_of(int units, long long tokens, int d, int run) {
+Plan plan_of(int units, long long tokens, int d, int run, int most_ctas) {
     auto space = [run](int dd) { return S(dd, row_lanes(dd), run); };
     Plan p{1, 0, 0, space(d).tokens};
     long long least = -1;
     for (int r = 1; r <= kMostRanks; ++r) {
         const int smem = space(d).bytes(r);
-        const long long slots = (2 * (smem + 2048) <= 228 * 1024 ? 2 : 1) * (long long)sm_count();
+        const long long slots = (2 * (smem + 2048) <= 228 * 1024 ? most_ctas : 1) * (long long)sm_count();
         const long long rounds = ((long long)units * r + slots - 1) / slots, stride = (long long)r * p.chunk;
         const long long cost = rounds * ((tokens + stride - 1) / stride + 2);
         if (least < 0 || cost < least) {
@@ -1198,14 +1239,14 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
             return cudaGetLastError();
         }
         constexpr int run = forward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run);
+        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run, 2);
         RowMap v = {}, g = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
             if (e == cudaSuccess && K::CHAN) e = row_map(&g, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
-        return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC>>(
+        return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC, K::LANES>>(
             32 * kForwardWarps + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, lanes, every);
     });
 }
@@ -1218,7 +1259,7 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
         using In = typename K::In;
         using Out = typename K::Out;
         constexpr int run = backward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run);
+        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run, K::LANES > 0 ? 2 : 1);
         RowMap v = {}, y = {}, gate = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
@@ -1227,7 +1268,7 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
             if (e == cudaSuccess && K::CHAN) e = row_map(&gate, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
-        return launch_clusters<scan_backward_kernel<In, Out, K::CHAN, K::VEC>>(
+        return launch_clusters<scan_backward_kernel<In, Out, K::CHAN, K::VEC, K::LANES>>(
             32 * kBackwardWarps + 32, units, p.ranks, p.smem, p.most, s, a, g, v, y, gate, c.heads, units, c.d, lanes);
     });
 }
