@@ -21,10 +21,10 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
 // for each CTA and each of q and k.
 constexpr int kQkPartials = 1024;
 
-cudaError_t launch_qk_norm(const lq_qk_norm_config &c, const lq_qk_norm_args &a, const lq_qk_pair &out,
+cudaError_t launch_qk_norm(const lq_qk_norm_config &c, const lq_qk_norm_args &a, const lq_qk_pair &out, bool vec,
                            cudaStream_t s);
 cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm_args &a, const lq_qk_pair &grad_out,
                                     const lq_qk_pair &grad_in, float *grad_wq, float *grad_wk, float *partials,
-                                    cudaStream_t s);
+                                    bool vec, cudaStream_t s);
 
 }  // namespace lq

@@ -102,6 +102,17 @@ const char *why_not(const lq_qk_norm_config &c, int64_t n_tokens, const lq_qk_pa
     return nullptr;
 }
 
+// Whether every row of q and k is whole, aligned pieces of 16 bytes.
+bool rows_of_16_bytes(const lq_qk_norm_config &c, const void *q, const void *k, int64_t q_token, int64_t q_head,
+                      int64_t k_token, int64_t k_head) {
+    const int64_t m = (int64_t)(16 / element(c.dtype));
+    const bool keys = c.heads_k == 0 || (aligned(k, 16) && k_token % m == 0 && k_head % m == 0);
+    return c.d % m == 0 && aligned(q, 16) && q_token % m == 0 && q_head % m == 0 && keys;
+}
+bool rows_of_16_bytes(const lq_qk_norm_config &c, const lq_qk_pair &p) {
+    return rows_of_16_bytes(c, p.q, p.k, p.q_token, p.q_head, p.k_token, p.k_head);
+}
+
 }  // namespace
 
 extern "C" {
@@ -162,7 +173,9 @@ lq_status lq_qk_norm_rotate(const lq_qk_norm_config *cfg, const lq_qk_norm_args 
     if (const char *why = why_not(cfg)) return fail(LQ_ERR_INVALID_ARG, why);
     if (const char *why = why_not(*cfg, args)) return fail(LQ_ERR_INVALID_ARG, why);
     if (const char *why = why_not(*cfg, args->n_tokens, out, true)) return fail(LQ_ERR_INVALID_ARG, why);
-    const cudaError_t e = lq::launch_qk_norm(*cfg, *args, *out, static_cast<cudaStream_t>(stream));
+    const bool vec = rows_of_16_bytes(*cfg, args->q, args->k, args->q_token, args->q_head, args->k_token, args->k_head) &&
+                     rows_of_16_bytes(*cfg, *out);
+    const cudaError_t e = lq::launch_qk_norm(*cfg, *args, *out, vec, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LQ_OK : cuda_fail(e, "launching the norm kernel");
 }
 
@@ -188,8 +201,11 @@ lq_status lq_qk_norm_rotate_backward(const lq_qk_norm_config *cfg, const lq_qk_n
         return fail(LQ_ERR_INVALID_ARG, "a pointer is not aligned to its element");
     if ((grad_weight_q != nullptr || grad_weight_k != nullptr) && (workspace == nullptr || !aligned(workspace, 16)))
         return fail(LQ_ERR_WORKSPACE, "a weight gradient needs a 16-byte aligned workspace");
+    const bool vec = rows_of_16_bytes(*cfg, args->q, args->k, args->q_token, args->q_head, args->k_token, args->k_head) &&
+                     rows_of_16_bytes(*cfg, *grad_out) && rows_of_16_bytes(*cfg, *grad_in);
     const cudaError_t e = lq::launch_qk_norm_backward(*cfg, *args, *grad_out, *grad_in, grad_weight_q, grad_weight_k,
-                                                      static_cast<float *>(workspace), static_cast<cudaStream_t>(stream));
+                                                      static_cast<float *>(workspace), vec,
+                                                      static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LQ_OK : cuda_fail(e, "launching the norm's backward kernel");
 }
 

@@ -75,7 +75,7 @@ def test_checkpoints_are_small_and_grow_with_the_tokens(d):
     L, cfg = lq.lib(), scan_config(d=d)
     size = [L.lq_gated_scan_checkpoint_bytes(ref(cfg), n) for n in (0, 1, 32, 33, 4096, 1 << 20)]
     assert size[0] == 0 and size[1] == 6 * d * 4 and size == sorted(size)
-    assert size[-1] <= (1 << 20) // 32 * 6 * d * 4
+    assert size[-1] <= -(-(1 << 20) // 24) * 6 * d * 4       # at least 24 tokens apart: 6 warps' rows of 4 tokens
     assert L.lq_gated_scan_checkpoint_bytes(ref(cfg), -1) == 0
 
 
