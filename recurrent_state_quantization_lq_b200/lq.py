@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -203,67 +204,87 @@ def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
 
 
 # ------------------------------------------------------- stateless operators
+# The structs above as packed bytes (a call's own, so threads share nothing):
+# filling a ctypes struct takes longer than a small kernel runs.
+_pack_scan_config = struct.Struct("6i").pack
+_pack_scan_args = struct.Struct("2i8P12q").pack
+_pack_scan_grads = struct.Struct("6P12q").pack
+_pack_qk_config = struct.Struct("7i2f").pack
+_pack_qk_args = struct.Struct("q6P4q").pack
+_pack_qk_pair = struct.Struct("2P4q").pack
+_NO_STRIDES = (0, 0, 0)
+
+
 def _on(x: torch.Tensor, stream):
     """None when `x`'s device and the given stream are the current ones; else
     the context that makes them so, for the launch and what it allocates."""
     assert x.is_cuda, "a CUDA tensor is needed"
     if stream is None:
-        return None if x.device.index == torch.cuda.current_device() else torch.cuda.device(x.device)
+        return None if x.get_device() == torch.cuda.current_device() else torch.cuda.device(x.device)
     assert stream.device == x.device, (stream.device, x.device)
     return torch.cuda.stream(stream)
 
 
-def _tensor(x: torch.Tensor | None, what: str, like: torch.Tensor, dtype, shape, packed: bool = True):
-    """Check one tensor argument (None is a NULL pointer) and return its address."""
+# the current stream's handle without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _refuse(x: torch.Tensor, what: str, device: int, dtype, shape):
+    raise AssertionError(f"{what}: {x.dtype} {tuple(x.shape)} with strides {x.stride()} on device {x.get_device()}; "
+                         f"wanted {dtype} {tuple(shape)} on device {device}, contiguous (rows: their channels)")
+
+
+def _packed(x: torch.Tensor | None, what: str, device: int, dtype, shape) -> int:
+    """The address of a contiguous tensor argument (0: None)."""
     if x is None:
-        return None
-    assert x.device == like.device, (what, x.device, like.device)
-    assert x.dtype == dtype, (what, x.dtype, dtype)
-    assert x.shape == shape, (what, tuple(x.shape), tuple(shape))
-    assert not packed or x.is_contiguous(), f"{what} must be contiguous"
+        return 0
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or not x.is_contiguous():
+        _refuse(x, what, device, dtype, shape)
     return x.data_ptr()
 
 
-def _rows(x: torch.Tensor | None, what: str, like: torch.Tensor, dtype, shape):
-    """Check a [T, batch, heads(, d)] tensor of any strides whose channels are
-    contiguous; its address and its Strides."""
+def _rows(x: torch.Tensor | None, what: str, device: int, dtype, shape):
+    """The address and strides of a [T, batch, heads(, d)] argument of any
+    strides whose channels are contiguous."""
     if x is None:
-        return None, (0, 0, 0)
-    p = _tensor(x, what, like, dtype, shape, packed=False)
+        return 0, _NO_STRIDES
     s = x.stride()
-    assert len(s) == 3 or s[3] == 1 or shape[3] == 1, f"{what}: channels must be contiguous"
-    return p, s[:3]
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or (len(s) == 4 and s[3] != 1 != shape[3]):
+        _refuse(x, what, device, dtype, shape)
+    return x.data_ptr(), s[:3]
 
 
-def _scan_config(v: torch.Tensor, g: torch.Tensor, out_dtype) -> ScanConfig:
+def _scan_config(v: torch.Tensor, g: torch.Tensor, out_dtype) -> bytes:
     assert v.dim() == 4, "v is [T, batch, heads, d]"
-    assert g.shape == v.shape or g.shape == v.shape[:3], "g is [T, batch, heads] or [T, batch, heads, d]"
     T, B, H, d = v.shape
-    return ScanConfig(B, H, d, int(g.dim() == 4), DTYPE[v.dtype], DTYPE[out_dtype])
+    chan = g.dim() == 4
+    assert g.shape == (v.shape if chan else (T, B, H)), "g is [T, batch, heads] or [T, batch, heads, d]"
+    return _pack_scan_config(B, H, d, chan, DTYPE[v.dtype], DTYPE[out_dtype])
 
 
 def gated_scan_checkpoints(v: torch.Tensor, g: torch.Tensor) -> torch.Tensor:
     """The buffer that gated_scan(checkpoints=) fills for gated_scan_backward()
     on inputs of these shapes."""
-    cfg = _scan_config(v, g, v.dtype)
-    n = lib().lq_gated_scan_checkpoint_bytes(ctypes.byref(cfg), v.shape[0])
+    n = lib().lq_gated_scan_checkpoint_bytes(_scan_config(v, g, v.dtype), v.shape[0])
     if n == 0 and v.shape[0] > 0:
         raise LQError(LQ_ERR_INVALID_ARG, "lq_gated_scan_checkpoint_bytes")
-    return torch.empty(n // 4, dtype=torch.float32, device=v.device)
+    return v.new_empty(n // 4, dtype=torch.float32)
 
 
-def _scan_args(v, g, beta, lengths, checkpoints, out_dtype):
-    cfg = _scan_config(v, g, out_dtype)
-    T, B, H, d = v.shape
-    pv, sv = _rows(v, "v", v, v.dtype, v.shape)
-    pg, sg = _rows(g, "g", v, torch.float32, g.shape)
-    pb, sb = _rows(beta, "beta", v, torch.float32, v.shape[:3])
-    pl = _tensor(lengths, "lengths", v, torch.int32, (B,))
-    if checkpoints is not None:
-        n = lib().lq_gated_scan_checkpoint_bytes(ctypes.byref(cfg), T) // 4
-        assert checkpoints.numel() >= n, "checkpoints of another shape: see gated_scan_checkpoints()"
-    pc = _tensor(checkpoints, "checkpoints", v, torch.float32, () if checkpoints is None else checkpoints.shape)
-    return cfg, ScanArgs(T, 0, pv, pg, pb, None, pl, None, None, pc, sv, sg, sb, (0, 0, 0))
+def _scan_inputs(v, g, beta, lengths, checkpoints, cfg, device):
+    """Addresses of v, g, beta, lengths and checkpoints, and the strides of the first three."""
+    T, B, H, _ = v.shape
+    pv, sv = _rows(v, "v", device, v.dtype, v.shape)
+    pg, sg = _rows(g, "g", device, torch.float32, g.shape)
+    pb, sb = _rows(beta, "beta", device, torch.float32, (T, B, H))
+    pl = _packed(lengths, "lengths", device, torch.int32, (B,))
+    if checkpoints is None:
+        return pv, pg, pb, pl, 0, sv, sg, sb
+    need = lib().lq_gated_scan_checkpoint_bytes(cfg, T) // 4
+    assert checkpoints.numel() >= need, "checkpoints of another shape: see gated_scan_checkpoints()"
+    pc = _packed(checkpoints, "checkpoints", device, torch.float32, checkpoints.shape)
+    return pv, pg, pb, pl, pc, sv, sg, sb
 
 
 def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None, checkpoints=None, out_dtype=None,
@@ -283,17 +304,19 @@ def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None,
         with on:
             return gated_scan(v, g, beta, h0, lengths=lengths, out=out, h_last=h_last, checkpoints=checkpoints,
                               out_dtype=out_dtype, want_out=want_out)
+    device, states = v.get_device(), v.shape[1:]
     out_dtype = out.dtype if out is not None else out_dtype or v.dtype
-    cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
-    if out is None and want_out:
+    cfg = _scan_config(v, g, out_dtype)
+    pv, pg, pb, pl, pc, sv, sg, sb = _scan_inputs(v, g, beta, lengths, checkpoints, cfg, device)
+    zero_past = out is None
+    if zero_past and want_out:
         out = torch.empty_like(v, dtype=out_dtype)
-        args.zero_past = 1
     if h_last is None:
-        h_last = torch.empty(v.shape[1:], dtype=torch.float32, device=v.device)
-    args.h0 = _tensor(h0, "h0", v, torch.float32, v.shape[1:])
-    args.h_last = _tensor(h_last, "h_last", v, torch.float32, v.shape[1:])
-    args.out, args.out_stride = _rows(out, "out", v, out_dtype, v.shape)
-    st = lib().lq_gated_scan(ctypes.byref(cfg), ctypes.byref(args), _stream_ptr(None, v.device))
+        h_last = v.new_empty(states, dtype=torch.float32)
+    po, so = _rows(out, "out", device, out_dtype, v.shape)
+    args = _pack_scan_args(v.shape[0], zero_past, pv, pg, pb, _packed(h0, "h0", device, torch.float32, states), pl, po,
+                           _packed(h_last, "h_last", device, torch.float32, states), pc, *sv, *sg, *sb, *so)
+    st = lib().lq_gated_scan(cfg, args, _raw_stream(device))
     if st != LQ_OK:
         raise LQError(st, "lq_gated_scan")
     return out, h_last
@@ -313,73 +336,76 @@ def gated_scan_backward(grad_out, v, g, beta=None, *, checkpoints, grad_last=Non
             return gated_scan_backward(grad_out, v, g, beta, checkpoints=checkpoints, grad_last=grad_last,
                                        lengths=lengths, grad_v=grad_v, grad_g=grad_g, grad_beta=grad_beta,
                                        grad_h0=grad_h0)
+    device, states = v.get_device(), v.shape[1:]
     out_dtype = v.dtype if grad_out is None else grad_out.dtype
-    cfg, args = _scan_args(v, g, beta, lengths, checkpoints, out_dtype)
-    new = torch.empty_like
-    if lengths is not None:                    # rows past a length: by the kernel, unless a given tensor keeps its own
-        if grad_v is None and grad_g is None and grad_beta is None:
-            args.zero_past = 1
-        else:
-            new = torch.zeros_like
+    cfg = _scan_config(v, g, out_dtype)
+    pv, pg, pb, pl, pc, sv, sg, sb = _scan_inputs(v, g, beta, lengths, checkpoints, cfg, device)
+    # rows past a length: zeroed by the kernel, unless a given tensor is to keep its own
+    zero_past = grad_v is None and grad_g is None and grad_beta is None
+    new = torch.empty_like if zero_past or lengths is None else torch.zeros_like
     grad_v = new(v) if grad_v is None else grad_v
     grad_g = new(g) if grad_g is None else grad_g
     if beta is not None and grad_beta is None:
         grad_beta = new(beta)
     if grad_h0 is None:
-        grad_h0 = torch.empty(v.shape[1:], dtype=torch.float32, device=v.device)
-    grads = ScanGrads()
-    grads.grad_out, grads.grad_out_stride = _rows(grad_out, "grad_out", v, out_dtype, v.shape)
-    grads.grad_v, grads.grad_v_stride = _rows(grad_v, "grad_v", v, v.dtype, v.shape)
-    grads.grad_g, grads.grad_g_stride = _rows(grad_g, "grad_g", v, torch.float32, g.shape)
-    grads.grad_beta, grads.grad_beta_stride = _rows(grad_beta, "grad_beta", v, torch.float32, v.shape[:3])
-    grads.grad_last = _tensor(grad_last, "grad_last", v, torch.float32, v.shape[1:])
-    grads.grad_h0 = _tensor(grad_h0, "grad_h0", v, torch.float32, v.shape[1:])
-    st = lib().lq_gated_scan_backward(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(grads),
-                                      _stream_ptr(None, v.device))
+        grad_h0 = v.new_empty(states, dtype=torch.float32)
+    py, sy = _rows(grad_out, "grad_out", device, out_dtype, v.shape)
+    pgv, sgv = _rows(grad_v, "grad_v", device, v.dtype, v.shape)
+    pgg, sgg = _rows(grad_g, "grad_g", device, torch.float32, g.shape)
+    pgb, sgb = _rows(grad_beta, "grad_beta", device, torch.float32, v.shape[:3])
+    args = _pack_scan_args(v.shape[0], zero_past, pv, pg, pb, 0, pl, 0, 0, pc, *sv, *sg, *sb, 0, 0, 0)
+    grads = _pack_scan_grads(py, _packed(grad_last, "grad_last", device, torch.float32, states), pgv, pgg, pgb,
+                             _packed(grad_h0, "grad_h0", device, torch.float32, states), *sy, *sgv, *sgg, *sgb)
+    st = lib().lq_gated_scan_backward(cfg, args, grads, _raw_stream(device))
     if st != LQ_OK:
         raise LQError(st, "lq_gated_scan_backward")
     return grad_v, grad_g, grad_beta, grad_h0
 
 
-def _heads_of(x: torch.Tensor, what: str, like: torch.Tensor, lead) -> tuple:
-    """Check a [..., heads, d] tensor; its address, token stride and head stride."""
-    assert x.device == like.device and x.dtype == like.dtype, (what, x.device, x.dtype)
-    assert x.dim() >= 2 and x.shape[:-2] == lead and x.shape[-1] == like.shape[-1], (what, tuple(x.shape))
+def _heads_of(x: torch.Tensor | None, what: str, device: int, dtype, shape):
+    """The address, token stride and head stride of a [..., heads, d] argument."""
+    if x is None:
+        return 0, 0, 0
     s = x.stride()
-    assert s[-1] == 1 or x.shape[-1] == 1, f"{what}: channels must be contiguous"
-    token, n = 0, 1
-    for size, step in zip(reversed(lead), reversed(s[:-2])):      # the tokens lie at one stride
-        if size == 1:
-            continue
-        if n == 1:
-            token = step
-        assert n == 1 or step == token * n, f"{what}: its leading dimensions are not one run of tokens"
-        n *= size
-    return x.data_ptr(), token, s[-2] if x.shape[-2] > 1 else x.shape[-1]
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != device or s[-1] != 1 != shape[-1]:
+        _refuse(x, what, device, dtype, shape)
+    if len(s) == 3:
+        token = s[0]
+    else:                                      # the tokens of several leading dimensions lie at one stride
+        token, n = 0, 1
+        for size, step in zip(reversed(shape[:-2]), reversed(s[:-2])):
+            if size == 1:
+                continue
+            token = step if n == 1 else token
+            assert step == token * n, f"{what}: its leading dimensions are not one run of tokens"
+            n *= size
+    # a dimension of one entry may have any stride: it is none
+    return x.data_ptr(), token, s[-2] if shape[-2] > 1 else shape[-1]
 
 
-def _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale):
-    lead, d = q.shape[:-2], q.shape[-1]
-    n = q.shape[:-2].numel()
-    heads_k = 0 if k is None else k.shape[-2]
+def _qk_inputs(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale):
+    """The packed config and args of a call."""
+    device, lead, d, dtype = q.get_device(), q.shape[:-2], q.shape[-1], q.dtype
+    assert k is None or (k.shape[:-2] == lead and k.dim() >= 2 and k.shape[-1] == d), "k is [..., heads_k, d], as q"
+    pq, tq, hq = _heads_of(q, "q", device, dtype, q.shape)
+    pk, tk, hk = _heads_of(k, "k", device, dtype, None if k is None else k.shape)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    cfg = QkNormConfig(q.shape[-2], heads_k, d, NORM[norm], rot, PAIRS[pairs], DTYPE[q.dtype], eps, q_scale)
-    pq, tq, hq = _heads_of(q, "q", q, lead)
-    pk, tk, hk = (None, 0, 0) if k is None else _heads_of(k, "k", q, lead)
-    if rot:
-        assert positions is not None, "a rotation needs positions"
-    return cfg, QkNormArgs(n, pq, pk, _tensor(positions, "positions", q, torch.int32, lead) if rot else None,
-                           _tensor(inv_freq, "inv_freq", q, torch.float64, (rot // 2,)),
-                           _tensor(weight_q, "weight_q", q, torch.float32, (d,)),
-                           _tensor(weight_k, "weight_k", q, torch.float32, (d,)), tq, hq, tk, hk)
+    assert rot == 0 or positions is not None, "a rotation needs positions"
+    cfg = _pack_qk_config(q.shape[-2], 0 if k is None else k.shape[-2], d, NORM[norm], rot, PAIRS[pairs], DTYPE[dtype],
+                          eps, q_scale)
+    args = _pack_qk_args(lead.numel(), pq, pk, _packed(positions, "positions", device, torch.int32, lead) if rot else 0,
+                         _packed(inv_freq, "inv_freq", device, torch.float64, (rot // 2,)),
+                         _packed(weight_q, "weight_q", device, torch.float32, (d,)),
+                         _packed(weight_k, "weight_k", device, torch.float32, (d,)), tq, hq, tk, hk)
+    return cfg, args
 
 
-def _qk_pair(q, k, like_q, like_k, what) -> QkPair:
-    assert q.shape == like_q.shape and (k is None) == (like_k is None) and (k is None or k.shape == like_k.shape), what
-    lead = like_q.shape[:-2]
-    pq, tq, hq = _heads_of(q, what, like_q, lead)
-    pk, tk, hk = (None, 0, 0) if k is None else _heads_of(k, what, like_q, lead)
-    return QkPair(pq, pk, tq, hq, tk, hk)
+def _qk_pair(q, k, like_q, like_k, what) -> bytes:
+    assert (k is None) == (like_k is None), what
+    device, dtype = like_q.get_device(), like_q.dtype
+    pq, tq, hq = _heads_of(q, what, device, dtype, like_q.shape)
+    pk, tk, hk = _heads_of(k, what, device, dtype, None if k is None else like_k.shape)
+    return _pack_qk_pair(pq, pk, tq, hq, tk, hk)
 
 
 def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, weight_k=None, norm: str = "l2",
@@ -397,12 +423,12 @@ def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, w
         with on:
             return qk_norm_rotate(q, k, positions=positions, inv_freq=inv_freq, weight_q=weight_q, weight_k=weight_k,
                                   norm=norm, eps=eps, pairs=pairs, q_scale=q_scale, q_out=q_out, k_out=k_out)
-    cfg, args = _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    cfg, args = _qk_inputs(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
+    if q_out is None:
+        q_out = q.new_empty(q.shape)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    out = _qk_pair(q_out, k_out, q, k, "an output")
-    st = lib().lq_qk_norm_rotate(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(out), _stream_ptr(None, q.device))
+        k_out = k.new_empty(k.shape)
+    st = lib().lq_qk_norm_rotate(cfg, args, _qk_pair(q_out, k_out, q, k, "an output"), _raw_stream(q.get_device()))
     if st != LQ_OK:
         raise LQError(st, "lq_qk_norm_rotate")
     return q_out, k_out
@@ -421,22 +447,22 @@ def qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k=None, *, positions=None
             return qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k, positions=positions, inv_freq=inv_freq,
                                            weight_q=weight_q, weight_k=weight_k, norm=norm, eps=eps, pairs=pairs,
                                            q_scale=q_scale, grad_q=grad_q, grad_k=grad_k)
-    cfg, args = _qk_args(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
-    gy = _qk_pair(grad_q_out, grad_k_out, q, k, "a gradient of an output")
-    grad_q = torch.empty(q.shape, dtype=q.dtype, device=q.device) if grad_q is None else grad_q
+    cfg, args = _qk_inputs(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
+    if grad_q is None:
+        grad_q = q.new_empty(q.shape)
     if k is not None and grad_k is None:
-        grad_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    gx = _qk_pair(grad_q, grad_k, q, k, "a gradient of an input")
+        grad_k = k.new_empty(k.shape)
     gwq = None if weight_q is None else torch.empty_like(weight_q)
     gwk = None if weight_k is None else torch.empty_like(weight_k)
     work = None
     if gwq is not None or gwk is not None:
-        n = lib().lq_qk_norm_rotate_workspace_bytes(ctypes.byref(cfg))
+        n = lib().lq_qk_norm_rotate_workspace_bytes(cfg)
         if n == 0:
             raise LQError(LQ_ERR_INVALID_ARG, "lq_qk_norm_rotate_workspace_bytes")
-        work = torch.empty(n, dtype=torch.uint8, device=q.device)
-    st = lib().lq_qk_norm_rotate_backward(ctypes.byref(cfg), ctypes.byref(args), ctypes.byref(gy), ctypes.byref(gx),
-                                          _ptr(gwq), _ptr(gwk), _ptr(work), _stream_ptr(None, q.device))
+        work = q.new_empty(n, dtype=torch.uint8)
+    st = lib().lq_qk_norm_rotate_backward(cfg, args, _qk_pair(grad_q_out, grad_k_out, q, k, "a gradient of an output"),
+                                          _qk_pair(grad_q, grad_k, q, k, "a gradient of an input"), _ptr(gwq), _ptr(gwk),
+                                          _ptr(work), _raw_stream(q.get_device()))
     if st != LQ_OK:
         raise LQError(st, "lq_qk_norm_rotate_backward")
     return grad_q, grad_k, gwq, gwk
@@ -448,12 +474,20 @@ class DecodeState:
     The workspace is a torch uint8 tensor on ``device``; its regions can be
     viewed with :meth:`view`.  All calls enqueue on ``stream`` (default: the
     current stream) and return without synchronizing.
+
+    ``qk_norm``: keywords of :func:`qk_norm_rotate` (norm, weights, inv_freq,
+    q_scale, ...; {} for the plain L2 norm).  The decode and prefill calls then
+    take q and k as a projection gives them (any strides that it takes) and
+    normalise and rotate them first; with inv_freq they want ``positions``
+    int32 [batch], or [T, batch] for a prompt.  The rows of sequences that are
+    inactive or not masked are then read too, and never used.
     """
 
     def __init__(self, batch: int, heads: int, d: int, *, window: int = 64, n_comp_rows: int = 2,
                  n_comp_cols: int = 2, gate: str = "scalar", mode: str = "window", smooth: int = 1,
                  select: str = "l2", in_dtype: torch.dtype = torch.bfloat16, ragged: bool = False,
-                 device=None):
+                 device=None, qk_norm: dict | None = None):
+        self.qk_norm = qk_norm
         self.cfg = make_config(batch, heads, d, window, n_comp_rows, n_comp_cols, gate, mode, smooth,
                                select, in_dtype, ragged)
         self.ragged = bool(ragged)
@@ -487,10 +521,18 @@ class DecodeState:
         self._check(lib().lq_prefill_state(self._h, _ptr(S0), _stream_ptr(stream, self.device)),
                     "lq_prefill_state")
 
+    def _normed(self, q, k, positions, stream):
+        """q and k as the C ABI takes them: through qk_norm where the state has one."""
+        if self.qk_norm is None:
+            assert positions is None, "positions without qk_norm"
+            return q, k
+        return qk_norm_rotate(q, k, positions=positions, stream=stream, **self.qk_norm)
+
     def decode_step(self, q, k, v, g, beta, out: torch.Tensor | None = None, stream=None,
-                    active: torch.Tensor | None = None) -> torch.Tensor:
+                    active: torch.Tensor | None = None, positions: torch.Tensor | None = None) -> torch.Tensor:
         """One token for every sequence; on a ragged state, for the sequences
         with active[b] != 0 (uint8 [batch] on the device; None = all)."""
+        q, k = self._normed(q, k, positions, stream)
         if out is None:
             out = torch.empty(self.batch, self.heads, self.d, dtype=torch.float32, device=self.device)
         for t, dt in ((q, self.in_dtype), (k, self.in_dtype), (v, self.in_dtype), (g, torch.float32),
@@ -526,11 +568,12 @@ class DecodeState:
                     "lq_prefill_sequences")
 
     def prefill_tokens(self, q, k, v, g, beta, S0: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                       stream=None) -> torch.Tensor | None:
+                       stream=None, positions: torch.Tensor | None = None) -> torch.Tensor | None:
         """Run the FP32 recurrence over a prompt (inputs [T, batch, heads, ...]
         as for decode_step, stacked over tokens) from S0 (None = zero state) and
         encode its final state as the window-start state.  Writes the prompt's
         outputs into `out` ([T, batch, heads, d] FP32) when given."""
+        q, k = self._normed(q, k, positions, stream)
         T = q.shape[0]
         for t, dt in ((q, self.in_dtype), (k, self.in_dtype), (v, self.in_dtype), (g, torch.float32),
                       (beta, torch.float32)):
@@ -547,10 +590,11 @@ class DecodeState:
 
     def prefill_sequences_tokens(self, q, k, v, g, beta, mask: torch.Tensor, lengths: torch.Tensor | None = None,
                                  S0: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                                 stream=None) -> torch.Tensor | None:
+                                 stream=None, positions: torch.Tensor | None = None) -> torch.Tensor | None:
         """Ragged: restart the sequences with mask[b] != 0 from S0 (None = zero)
         through their prompts: inputs [T, batch, heads, ...] padded to T tokens,
         lengths int32 [batch] on the device (None = T for every sequence)."""
+        q, k = self._normed(q, k, positions, stream)
         T = q.shape[0]
         for t, dt in ((q, self.in_dtype), (k, self.in_dtype), (v, self.in_dtype), (g, torch.float32),
                       (beta, torch.float32)):

@@ -136,6 +136,22 @@ def test_the_binding_refuses_host_tensors():
             call()
 
 
+def test_packed_structs_are_the_structs():
+    """The binding packs its calls with formats of the structs' sizes."""
+    import struct
+    for pack, cls in ((lq._pack_scan_config, lq.ScanConfig), (lq._pack_scan_args, lq.ScanArgs),
+                      (lq._pack_scan_grads, lq.ScanGrads), (lq._pack_qk_config, lq.QkNormConfig),
+                      (lq._pack_qk_args, lq.QkNormArgs), (lq._pack_qk_pair, lq.QkPair)):
+        f = pack.__self__
+        assert f.size == ctypes.sizeof(cls)
+        values = [i + 1 for i in range(len(struct.unpack(f.format, bytes(f.size))))]
+        flat, got = [], cls.from_buffer_copy(pack(*values))
+        for n, t in cls._fields_:
+            x = getattr(got, n)
+            flat += [getattr(x, m) for m, _ in t._fields_] if t is lq.Strides else [x]
+        assert flat == values, cls
+
+
 def test_structs_match_the_header():
     """Field names and order of the binding's structs are the header's."""
     import re
