@@ -182,6 +182,7 @@ __host__ __device__ inline int box_of(int tokens) {
 __device__ __forceinline__ void bring_boxes(unsigned char *base, const RowMap &m, const Unit &w, int t_first, int tokens,
                                             int row_bytes, uint64_t *bar) {
     const int box = box_of(tokens);
+#pragma unroll 1
     for (int t = 0; t < tokens; t += box)
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
@@ -195,6 +196,7 @@ template <typename T>
 __device__ __forceinline__ void bring_row(unsigned char *base, int pitch, const T *src, int64_t token_stride, int first,
                                           int live, int c0, int n) {
     T *q = reinterpret_cast<T *>(base) + first * pitch + c0;
+#pragma unroll 1
     for (int i = 0; i < live; ++i, src += token_stride, q += pitch) {
         Raw8<T> r;
         load8<false>(src, n, r);
@@ -223,6 +225,12 @@ __device__ __forceinline__ void read_shared(const unsigned char *base, int pitch
     Raw8<T> r;
     read_shared(base, pitch, token, c0, r);
     widen8(r, x);
+}
+// Its first n channels (rounded up to 16 bytes) set to zero.
+template <typename T>
+__device__ __forceinline__ void clear_shared(unsigned char *base, int pitch, int token, int c0, int n) {
+    const float2 zero[4] = {};
+    store8<true>(reinterpret_cast<T *>(base) + token * pitch + c0, n, zero);
 }
 __device__ __forceinline__ void read_shared(const float *q, float2 *x) {
     Raw8<float> r;
@@ -489,11 +497,11 @@ __global__ void __launch_bounds__(kRowsThreads) scan_rows_kernel(lq_scan_args a,
 template <typename InT, bool CHAN>
 using ForwardSpace = Space<kForwardWarps, (int)sizeof(InT), CHAN ? 4 : 0, 0, CHAN, false>;
 
-template <typename InT, typename OutT, bool CHAN, bool VEC, int LANES>
+template <typename InT, typename OutT, bool CHAN, bool VEC, int D_>
 __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
     scan_forward_kernel(lq_scan_args a, const __grid_constant__ RowMap map_v, const __grid_constant__ RowMap map_g,
-                        int heads, int units, int d, int any_lanes, int every) {
-    const int lanes = LANES > 0 ? LANES : any_lanes;
+                        int heads, int units, int any_d, int every) {
+    const int d = D_ > 0 ? D_ : any_d, lanes = row_lanes(d);
     constexpr int R = forward_run(sizeof(InT) == 2, CHAN);
     constexpr int NW = kForwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -532,6 +540,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
                     if (CHAN) bring_boxes(base + gates_at, map_g, w, t_cta, chunk, d * 4, full);
                 }
             }
+#pragma unroll 1
             for (int i = lane; i < live; i += 32) {
                 if (!CHAN) cp_async4(&sc[i].x, pg + (t_cta + i) * a.g_stride.token);
                 if (pb != nullptr) cp_async4(&sc[i].y, pb + (t_cta + i) * a.beta_stride.token);
@@ -560,7 +569,6 @@ __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
         const int in_row = lane & (lanes - 1), c0 = in_row * 8, row = tid / lanes;
         const bool on = c0 < d;
         const int n = on ? min(8, d - c0) : 0, cr = on ? c0 : 0;     // (lanes past d run with others' channels)
-        const int last_row = (tid | 31) / lanes;                     // of the warp
         auto bring = [&](int s, int stage) {
             const int t_row = s * stride + rank * chunk + row * R, live = min(max(w.len - t_row, 0), R);
             unsigned char *base = smem + stage * space.stage();
@@ -588,35 +596,39 @@ __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
                 float *sH = maps + (s & 1) * space.map(), *sA = sH + NW * dp;
                 if (alive) alive = mbar_wait(&bars.full[one.stage], one.parity, kWaitBudgetCycles);
                 if (!alive) A.fill(nanf(""));
-                if (!CHAN) {                         // each gate is raised once, by one lane of its row
-                    for (int i = in_row; i < live; i += lanes) sc[i].x = gate_of(sc[i].x);
-                    __syncwarp();
+                // each gate is raised once, by one lane of its row; past the end it is 1, and beta 0
+                for (int i = in_row; i < R; i += lanes) {
+                    if (!CHAN) sc[i].x = i < live ? gate_of(sc[i].x) : 1.0f;
+                    if (i >= live) sc[i].y = 0.0f;
+                    else if (pb == nullptr) sc[i].y = 1.0f;
                 }
-                // FULL: every row of the warp has R tokens (a straight line of code)
-                auto pass = [&](auto FULL) {
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        if (!FULL && (i >= live || !on)) break;
-                        const float2 gb = sc[i];
-                        const float b = pb != nullptr ? gb.y : 1.0f;
-                        Gates<CHAN> gate;
-                        if constexpr (CHAN) {        // raised once: pass two finds alpha in its place
-                            float *g = reinterpret_cast<float *>(base + gates_at) + (row * R + i) * pitch + cr;
-                            read_shared(g, gate.a);
-                            gate.exponentiate();
-                            if (on) store8<true>(g, n, gate.a);
-                        } else {
-                            gate.fill(gb.x);
-                        }
-                        float2 v[4];
-                        read_shared<InT>(base, pitch, row * R + i, cr, v);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) H[c] = fma2(gate[c], H[c], mul2(make_float2(b, b), v[c]));
-                        A.times(gate);
+                __syncwarp();
+                if (live < R && on) {                // what lies past the sequence's end is nothing
+#pragma unroll 1
+                    for (int i = live; i < R; ++i) {
+                        clear_shared<InT>(base, pitch, row * R + i, c0, n);
+                        if (CHAN) clear_shared<float>(base + gates_at, pitch, row * R + i, c0, n);
                     }
-                };
-                if (s * stride + rank * chunk + (last_row + 1) * R <= w.len) pass(std::true_type());
-                else pass(std::false_type());
+                    fence_proxy_async_smem();
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float2 gb = sc[i];
+                    Gates<CHAN> gate;
+                    if constexpr (CHAN) {            // raised once: pass two finds alpha in its place
+                        float *g = reinterpret_cast<float *>(base + gates_at) + (row * R + i) * pitch + cr;
+                        read_shared(g, gate.a);
+                        gate.exponentiate();
+                        if (on) store8<true>(g, n, gate.a);
+                    } else {
+                        gate.fill(gb.x);
+                    }
+                    float2 v[4];
+                    read_shared<InT>(base, pitch, row * R + i, cr, v);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) H[c] = fma2(gate[c], H[c], mul2(make_float2(gb.y, gb.y), v[c]));
+                    A.times(gate);
+                }
                 for (int o = lanes; o < 32; o *= 2) {
                     const Gates<CHAN> before = A.before(o);
 #pragma unroll
@@ -656,26 +668,20 @@ __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
                         ++mark;
                     }
                 }
-                auto pass = [&](auto FULL) {
+                if (a.out != nullptr) {
                     OutT *po = static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t_row) + c0;
 #pragma unroll
                     for (int i = 0; i < R; ++i, po += a.out_stride.token) {
-                        if (!FULL && (i >= live || !on)) break;
                         const float2 gb = sc[i];
-                        const float b = pb != nullptr ? gb.y : 1.0f;
                         Gates<CHAN> gate;
                         if constexpr (CHAN) read_shared<float>(base + gates_at, pitch, row * R + i, cr, gate.a);
                         else gate.fill(gb.x);
                         float2 v[4];
                         read_shared<InT>(base, pitch, row * R + i, cr, v);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) h[c] = fma2(gate[c], h[c], mul2(make_float2(b, b), v[c]));
-                        if (!FULL || on) store8<VEC>(po, n, h);
+                        for (int c = 0; c < 4; ++c) h[c] = fma2(gate[c], h[c], mul2(make_float2(gb.y, gb.y), v[c]));
+                        if (i < live && on) store8<VEC>(po, n, h);
                     }
-                };
-                if (a.out != nullptr) {
-                    if ((s - 1) * stride + rank * chunk + (last_row + 1) * R <= w.len) pass(std::true_type());
-                    else pass(std::false_type());
                 }
                 if (!VEC && s - 1 + kStages < steps) bring(s - 1 + kStages, two.stage);
                 if (CHAN) fence_proxy_async_smem();  // alpha was written where the next copy lands
@@ -689,6 +695,7 @@ __global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
         }
         if (a.zero_past && a.out != nullptr && on) {
             const float2 zero[4] = {};
+#pragma unroll 1
             for (int t = w.len + rank * rows + row; t < a.n_tokens; t += ranks * rows)
                 store8<VEC>(static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t) + c0, n, zero);
         }
@@ -736,12 +743,12 @@ using BackwardSpace = Space<kBackwardWarps, (int)sizeof(InT), (int)sizeof(OutT),
 // cluster.  With h what enters the row from before and X from behind, P_t the
 // product of its gates up to t and Q_t of those after t, pass two has
 //     alpha_t h_{t-1} = P_t h + its local value,   D_t = Q_t X + its local value.
-template <typename InT, typename OutT, bool CHAN, bool VEC, int LANES>
-__global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
+template <typename InT, typename OutT, bool CHAN, bool VEC, int D_>
+__global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
     scan_backward_kernel(lq_scan_args a, lq_scan_grads g, const __grid_constant__ RowMap map_v,
                          const __grid_constant__ RowMap map_y, const __grid_constant__ RowMap map_g, int heads, int units,
-                         int d, int any_lanes) {
-    const int lanes = LANES > 0 ? LANES : any_lanes;
+                         int any_d) {
+    const int d = D_ > 0 ? D_ : any_d, lanes = row_lanes(d);
     constexpr int R = backward_run(sizeof(InT) == 2, CHAN);
     constexpr int NW = kBackwardWarps;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -783,6 +790,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
                 }
             }
             float2 *sc = reinterpret_cast<float2 *>(base + space.scalars());
+#pragma unroll 1
             for (int j = lane; j < live; j += 32) {
                 if (!CHAN) cp_async4(&sc[j].x, pg + (t_cta + j) * a.g_stride.token);
                 if (pb != nullptr) cp_async4(&sc[j].y, pb + (t_cta + j) * a.beta_stride.token);
@@ -790,6 +798,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
             float *mark = reinterpret_cast<float *>(base + space.mark());
             const float *from = a.checkpoints + ((int64_t)(t_cta / chunk) * units + w.u) * d;
             if (live > 0)
+#pragma unroll 1
                 for (int c = lane; c < d; c += 32) cp_async4(mark + c, from + c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -803,9 +812,11 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
             if (s + 1 < steps) asm volatile("cp.async.wait_group 1;" ::: "memory");      // step s + 1 may be on its way
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
             float2 *sc = reinterpret_cast<float2 *>(smem + now.stage * space.stage() + space.scalars());
-            for (int j = lane, live = live_of(s); j < live; j += 32) {                  // (the lane's own copies)
-                if (!CHAN) sc[j].x = gate_of(sc[j].x);
-                if (pb == nullptr) sc[j].y = 1.0f;
+#pragma unroll 1
+            for (int j = lane, live = live_of(s); j < chunk; j += 32) {      // (the lane's own copies)
+                if (!CHAN) sc[j].x = j < live ? gate_of(sc[j].x) : 1.0f;     // past the end: 1, and beta 0
+                if (j >= live) sc[j].y = 0.0f;
+                else if (pb == nullptr) sc[j].y = 1.0f;
             }
             mbar_arrive(&bars.full[now.stage]);
             next.next();
@@ -821,7 +832,6 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
         const int in_row = lane & (lanes - 1), c0 = in_row * 8, row = tid / lanes;
         const bool on = c0 < d;
         const int n = on ? min(8, d - c0) : 0, cr = on ? c0 : 0;     // (lanes past d run with others' channels)
-        const int last_row = (tid | 31) / lanes;                     // of the warp
         const int group = max(lanes, 8), in_group = lane & (group - 1), per_group = group / lanes;
         const int first = row & ~(per_group - 1), last = first + per_group - 1;      // rows of the group
         const int groups = 32 * NW / group, gate_row = space.gate_row(), peer = space.peer();
@@ -856,8 +866,8 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
         // A thread composes channel tid (and tid + 32 NW where there are as many);
         // where half of the threads are enough for the states, the other half
         // composes the gradients.
-        constexpr int NC = LANES > 0 && LANES <= 16 ? 1 : 2;
-        const int e_from = (LANES == 8 || (LANES == 0 && dp <= 16 * NW)) ? 16 * NW : 0;
+        constexpr int NC = D_ > 0 && D_ <= 32 * NW ? 1 : 2;
+        const int e_from = dp <= 16 * NW ? 16 * NW : 0;
         float carry[NC];             // what enters a step from behind
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
@@ -868,8 +878,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
         Turn turn;
         for (int s = 0; s < steps; ++s) {
             const int t_row = first_of(s) + row * R, live = min(max(w.len - t_row, 0), R);
-            const bool full_rows = first_of(s) + (last_row + 1) * R <= w.len;        // every row of the warp has R tokens
-            const unsigned char *base = smem + turn.stage * space.stage();
+            unsigned char *base = smem + turn.stage * space.stage();
             const float2 *sc = reinterpret_cast<const float2 *>(base + space.scalars()) + row * R;
             Gates<CHAN> P[R], Q[R], A, B;
             float2 ah[R][4], D[R][4], H[4] = {}, E[4] = {};
@@ -877,28 +886,32 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
             B.fill(1.0f);
             if (alive) alive = mbar_wait(&bars.full[turn.stage], turn.parity, kWaitBudgetCycles);
             if (!alive) A.fill(nanf(""));
-            auto pass = [&](auto FULL) {             // FULL: a straight line of code
+            if (live < R && on) {                    // what lies past the sequence's end is nothing
+#pragma unroll 1
+                for (int i = live; i < R; ++i) {
+                    clear_shared<InT>(base, pitch, row * R + i, c0, n);
+                    clear_shared<OutT>(base + y_at, pitch, row * R + i, c0, n);
+                    if (CHAN) clear_shared<float>(base + gates_at, pitch, row * R + i, c0, n);
+                }
+                fence_proxy_async_smem();
+            }
+            {
                 Gates<CHAN> gate[R];
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    float beta = 0.0f;
-                    float2 v[4] = {};
-                    gate[i].fill(1.0f);
-                    if (FULL || (i < live && on)) {
-                        const float2 gb = sc[i];
-                        beta = gb.y;
-                        if constexpr (CHAN) {
-                            read_shared<float>(base + gates_at, pitch, row * R + i, cr, gate[i].a);
-                            gate[i].exponentiate();
-                        } else {
-                            gate[i].fill(gb.x);
-                        }
-                        read_shared<InT>(base, pitch, row * R + i, cr, v);
+                    const float2 gb = sc[i];
+                    if constexpr (CHAN) {
+                        read_shared<float>(base + gates_at, pitch, row * R + i, cr, gate[i].a);
+                        gate[i].exponentiate();
+                    } else {
+                        gate[i].fill(gb.x);
                     }
+                    float2 v[4];
+                    read_shared<InT>(base, pitch, row * R + i, cr, v);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         ah[i][c] = mul2(gate[i][c], H[c]);
-                        H[c] = fma2(make_float2(beta, beta), v[c], ah[i][c]);
+                        H[c] = fma2(make_float2(gb.y, gb.y), v[c], ah[i][c]);
                     }
                     A.times(gate[i]);
                     P[i] = A;
@@ -906,7 +919,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
                     float2 y[4] = {};
-                    if ((FULL || (i < live && on)) && py != nullptr) read_shared<OutT>(base + y_at, pitch, row * R + i, cr, y);
+                    if (py != nullptr) read_shared<OutT>(base + y_at, pitch, row * R + i, cr, y);
                     Q[i] = B;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -915,9 +928,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
                     }
                     B.times(gate[i]);
                 }
-            };
-            if (full_rows) pass(std::true_type());
-            else pass(std::false_type());
+            }
             for (int o = lanes; o < group; o *= 2) {
                 const Gates<CHAN> ap = A.before(o), bp = B.after(o);
 #pragma unroll
@@ -1100,6 +1111,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
             }
         if (a.zero_past && on) {
             const float2 zero[4] = {};
+#pragma unroll 1
             for (int t = w.len + rank * rows + row; t < a.n_tokens; t += ranks * rows) {
                 if (g.grad_v != nullptr) store8<VEC>(static_cast<InT *>(g.grad_v) + row_of(g.grad_v_stride, w, t) + c0, n, zero);
                 if (CHAN && g.grad_g != nullptr) store8<VEC>(g.grad_g + row_of(g.grad_g_stride, w, t) + c0, n, zero);
@@ -1115,25 +1127,27 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, LANES > 0 ? 2 : 1)
 // ------------------------------------------------------------------ dispatch
 
 // A kernel's types and variants, as one value.
-template <typename In_, typename Out_, bool CHAN_, bool VEC_, int LANES_>
+template <typename In_, typename Out_, bool CHAN_, bool VEC_, int D_>
 struct Variant {
     using In = In_;
     using Out = Out_;
     static constexpr bool CHAN = CHAN_, VEC = VEC_;
-    static constexpr int LANES = LANES_;     // lanes of a row, where the kernel is compiled for them (0: any)
+    static constexpr int D = D_;             // channels, where the kernel is compiled for them (0: any)
 };
 
-// Rows of 16-byte pieces, one type in and out, are compiled for the lanes of
-// heads of 33..64, 65..128 and 129..256 channels: known strides save a dozen
-// registers, and a spilled one costs thousands of cycles a step here.
+// Aligned heads of 64, 128 and 256 channels, one type in and out, have kernels
+// of their own.  With the channels known, so is every place in shared memory:
+// registers were full before, and the places were worked out again at each use
+// (backward, composing took 3100 of 5850 cycles a step; one spilled register
+// cost thousands, the two CTAs of an SM leaving the L1 no room).
 template <typename In, typename Out, bool CHAN, typename F>
 cudaError_t by_rows(const lq_scan_config &c, bool vec, F &&f) {
     if constexpr (std::is_same<In, Out>::value) {
         if (vec) {
-            switch (row_lanes(c.d)) {
-                case 8: return f(Variant<In, Out, CHAN, true, 8>());
-                case 16: return f(Variant<In, Out, CHAN, true, 16>());
-                case 32: return f(Variant<In, Out, CHAN, true, 32>());
+            switch (c.d) {
+                case 64: return f(Variant<In, Out, CHAN, true, 64>());
+                case 128: return f(Variant<In, Out, CHAN, true, 128>());
+                case 256: return f(Variant<In, Out, CHAN, true, 256>());
                 default: break;
             }
         }
@@ -1246,20 +1260,20 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
             if (e == cudaSuccess && K::CHAN) e = row_map(&g, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
-        return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC, K::LANES>>(
-            32 * kForwardWarps + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, lanes, every);
+        return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC, K::D>>(
+            32 * kForwardWarps + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, every);
     });
 }
 
 cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a, const lq_scan_grads &g, bool vec,
                                  cudaStream_t s) {
-    const int units = c.batch * c.heads, lanes = row_lanes(c.d);
+    const int units = c.batch * c.heads;
     return by_variant(c, vec && a.n_tokens > 0, [&](auto k) {
         using K = decltype(k);
         using In = typename K::In;
         using Out = typename K::Out;
         constexpr int run = backward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run, K::LANES > 0 ? 2 : 1);
+        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run, K::D > 0 ? 2 : 1);
         RowMap v = {}, y = {}, gate = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
@@ -1268,8 +1282,8 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
             if (e == cudaSuccess && K::CHAN) e = row_map(&gate, a.g, a.g_stride, c, a.n_tokens, LQ_DTYPE_F32, p.chunk);
             if (e != cudaSuccess) return e;
         }
-        return launch_clusters<scan_backward_kernel<In, Out, K::CHAN, K::VEC, K::LANES>>(
-            32 * kBackwardWarps + 32, units, p.ranks, p.smem, p.most, s, a, g, v, y, gate, c.heads, units, c.d, lanes);
+        return launch_clusters<scan_backward_kernel<In, Out, K::CHAN, K::VEC, K::D>>(
+            32 * kBackwardWarps + 32, units, p.ranks, p.smem, p.most, s, a, g, v, y, gate, c.heads, units, c.d);
     });
 }
 

@@ -110,7 +110,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
 // Lanes that share a row of d channels, eight each: a power of two, 1..32.
-__host__ __device__ inline int row_lanes(int d) {
+__host__ __device__ constexpr int row_lanes(int d) {
     int l = 1;
     while (8 * l < d) l *= 2;
     return l;
