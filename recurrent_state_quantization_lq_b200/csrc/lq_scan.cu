@@ -974,8 +974,9 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
                         all_e = fmaf(a2, fmaf(a1, fmaf(a0, all_e, e0), e1), e2);
                         all_a *= a0 * a1 * a2;
                     }
-#pragma unroll 1
-                    for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+                    for (int r = 0; r < kMostRanks; ++r) {
+                        if (r >= ranks) break;
                         const uint32_t dst = peer_address(at, r), b = peer_address(bar, r);
                         peer_store(dst + c * 4, all_e, b);
                         if (CHAN || c == 0) peer_store(dst + (dp + c) * 4, all_a, b);
@@ -1215,11 +1216,13 @@ struct Plan {
     int ranks, smem, most, chunk;
 };
 
-// As many CTAs as take the fewest steps one after another, counting two steps'
-// time for the start and end of each round of CTAs on the device.  Registers
-// leave most_ctas CTAs to an SM, and shared memory one or two.
+// As many CTAs as take the least time: rounds of CTAs on the device, each its
+// steps and two more for its start and end, a step in a cluster costing
+// `shared` times one without (in hundredths: measured 115 forward, where the
+// exchange is hidden, and 160 backward).  Registers leave most_ctas CTAs to an
+// SM, and shared memory one or two.
 template <typename S>
-Plan plan_of(int units, long long tokens, int d, int run, int most_ctas) {
+Plan plan_of(int units, long long tokens, int d, int run, int most_ctas, int shared) {
     auto space = [run](int dd) { return S(dd, row_lanes(dd), run); };
     Plan p{1, 0, 0, space(d).tokens};
     long long least = -1;
@@ -1227,7 +1230,7 @@ Plan plan_of(int units, long long tokens, int d, int run, int most_ctas) {
         const int smem = space(d).bytes(r);
         const long long slots = (2 * (smem + 2048) <= 228 * 1024 ? most_ctas : 1) * (long long)sm_count();
         const long long rounds = ((long long)units * r + slots - 1) / slots, stride = (long long)r * p.chunk;
-        const long long cost = rounds * ((tokens + stride - 1) / stride + 2);
+        const long long cost = rounds * ((tokens + stride - 1) / stride + 2) * (r > 1 ? shared : 100);
         if (least < 0 || cost < least) {
             least = cost;
             p.ranks = r;
@@ -1253,7 +1256,7 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
             return cudaGetLastError();
         }
         constexpr int run = forward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run, 2);
+        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run, 2, 115);
         RowMap v = {}, g = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
@@ -1273,7 +1276,7 @@ cudaError_t launch_scan_backward(const lq_scan_config &c, const lq_scan_args &a,
         using In = typename K::In;
         using Out = typename K::Out;
         constexpr int run = backward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run, K::D > 0 ? 2 : 1);
+        const Plan p = plan_of<BackwardSpace<In, Out, K::CHAN>>(units, a.n_tokens, c.d, run, K::D > 0 ? 2 : 1, 160);
         RowMap v = {}, y = {}, gate = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
