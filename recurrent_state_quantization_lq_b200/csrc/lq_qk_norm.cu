@@ -38,8 +38,7 @@ __device__ __forceinline__ void angle_of(int position, double inv_freq, float *c
 // How a pair's two channels meet.
 enum { ROT_NONE, ROT_NEIGHBOURS, ROT_SHUFFLE, ROT_SHARED };
 
-// A thread's share of a row and, for the token it is at, its turns: channel i
-// of the eight becomes cs[i] u_i + sn[i] u_partner.
+// A thread's turns at a token: channel i of its eight becomes cs[i] u_i + sn[i] u_partner.
 template <int ROT>
 struct Turns {
     float cs[ROT == ROT_NONE ? 1 : 8], sn[ROT == ROT_NONE ? 1 : 8];
@@ -66,33 +65,64 @@ struct Turns {
             }
         }
     }
-    // Turn u (BACK: by the opposite angles).  row: the warp's rows in shared memory, [row][dp].
-    template <bool BACK>
-    __device__ __forceinline__ void turn(const lq_qk_norm_config &c, float *row, int c0, float *u) const {
-        if constexpr (ROT == ROT_NONE) return;
-        float p[8];
+    __device__ __forceinline__ static int partner_of(const lq_qk_norm_config &c, int e) {
+        const int half = c.rot_dim / 2;
+        return e >= c.rot_dim ? e : c.pairs == LQ_PAIRS_HALF ? (e < half ? e + half : e - half) : e ^ 1;
+    }
+    // The partners of a row's eight channels u, as they lie in `raw`.  row: the
+    // row's place in shared memory (ROT_SHARED).
+    template <typename T>
+    __device__ __forceinline__ void partners(const lq_qk_norm_config &c, const Raw8<T> &raw, const float2 *u, float *row,
+                                             int c0, float2 *p) const {
         if constexpr (ROT == ROT_NEIGHBOURS) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = u[i ^ 1];
+            for (int i = 0; i < 4; ++i) p[i] = make_float2(u[i].y, u[i].x);
+        } else if constexpr (ROT == ROT_SHUFFLE && sizeof(T) == 2) {     // half the shuffles: two channels a word
+            Raw8<T> r;
+            r.w.x = __shfl_sync(0xffffffffu, raw.w.x, partner);
+            r.w.y = __shfl_sync(0xffffffffu, raw.w.y, partner);
+            r.w.z = __shfl_sync(0xffffffffu, raw.w.z, partner);
+            r.w.w = __shfl_sync(0xffffffffu, raw.w.w, partner);
+            widen8(r, p);
         } else if constexpr (ROT == ROT_SHUFFLE) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, u[i], partner);
-        } else {
-            const int half = c.rot_dim / 2;
+            for (int i = 0; i < 4; ++i)
+                p[i] = make_float2(__shfl_sync(0xffffffffu, u[i].x, partner), __shfl_sync(0xffffffffu, u[i].y, partner));
+        } else if constexpr (ROT == ROT_SHARED) {
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[c0 + i] = u[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(row + c0 + 2 * i) = u[i];
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = c0 + i;
-                const int at = e >= c.rot_dim ? e : c.pairs == LQ_PAIRS_HALF ? (e < half ? e + half : e - half) : e ^ 1;
-                p[i] = row[at];
+            for (int i = 0; i < 4; ++i)
+                p[i] = make_float2(row[partner_of(c, c0 + 2 * i)], row[partner_of(c, c0 + 2 * i + 1)]);
+        }
+    }
+};
+
+// The linear part of a token's rows: y_i = C_i x_i + S_i x_partner.  Forward the
+// weights are in C and S, so that they cost a token's rows nothing; BACK is the
+// opposite turn.
+template <int ROT>
+struct Linear {
+    float2 C[4], S[ROT == ROT_NONE ? 1 : 4];
+    template <bool BACK>
+    __device__ __forceinline__ void set(const Turns<ROT> &t, const float *w, const float *w_partner) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float cs = ROT == ROT_NONE ? 1.0f : t.cs[ROT == ROT_NONE ? 0 : i];
+            (i & 1 ? C[i / 2].y : C[i / 2].x) = BACK ? cs : cs * w[i];
+            if constexpr (ROT != ROT_NONE) {
+                const float sn = t.sn[i];
+                (i & 1 ? S[i / 2].y : S[i / 2].x) = BACK ? -sn : sn * w_partner[i];
             }
         }
-        if constexpr (ROT != ROT_NONE) {
+    }
+    __device__ __forceinline__ void apply(const float2 *x, const float2 *p, float2 *y) const {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = fmaf(BACK ? -sn[i] : sn[i], p[i], cs[i] * u[i]);
+        for (int i = 0; i < 4; ++i) {
+            y[i] = mul2(C[i], x[i]);
+            if constexpr (ROT != ROT_NONE) y[i] = fma2(S[i], p[i], y[i]);
         }
     }
 };
@@ -117,147 +147,157 @@ __device__ __forceinline__ Share share_of(int d, int lanes, int split, int64_t g
     return s;
 }
 
-// One of q and k: a row's address and what its norm needs.
-struct Heads {
-    int n;                   // heads
-    float scale;
-    const float *weight;
-};
-
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_row(const T *p, const Share &s, Raw8<T> &r) {
     zero8(r);
     if (s.on) load8<VEC>(p, s.n, r);
 }
 
+// The weights of a thread's channels, and (forward) of their partners.
 __device__ __forceinline__ void load_weight(const float *w, const Share &s, float *x) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = w != nullptr && i < s.n ? __ldg(w + s.c0 + i) : 1.0f;
 }
-
-// r of a row whose eight channels are x.
-__device__ __forceinline__ float scale_of(const lq_qk_norm_config &c, const float *x, int lanes) {
-    float s = 0.0f;
+template <int ROT>
+__device__ __forceinline__ void load_partners(const lq_qk_norm_config &c, const float *w, const Share &s, float *x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-    for (int o = lanes / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return rsqrtf((c.norm == LQ_NORM_RMS ? s / (float)c.d : s) + c.eps);
+    for (int i = 0; i < 8; ++i)
+        x[i] = ROT != ROT_NONE && w != nullptr && i < s.n ? __ldg(w + Turns<ROT>::partner_of(c, s.c0 + i)) : 1.0f;
 }
 
-constexpr int kAhead = 4;    // rows in flight per thread, forward
+// The sum over a row of the products of two pairs' lists, and r from it.
+__device__ __forceinline__ float row_dot(const float2 *x, const float2 *y, int lanes) {
+    float2 t = mul2(x[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) t = fma2(x[i], y[i], t);
+    float s = t.x + t.y;
+    for (int o = lanes / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+__device__ __forceinline__ float scale_of(const lq_qk_norm_config &c, float sum, float mean_of) {
+    return rsqrtf(fmaf(sum, mean_of, c.eps));
+}
 
-template <typename T, bool VEC, int ROT>
-__global__ void __launch_bounds__(kQkThreads)
-    qk_norm_kernel(lq_qk_norm_config c, lq_qk_norm_args a, lq_qk_pair out, int lanes, int split) {
-    __shared__ float rows[ROT == ROT_SHARED ? kQkWarps * 32 * 8 : 1];
+// Rows in flight per thread.  Threads count for more than registers here: four
+// CTAs an SM with four rows (one, backward) take 135 us for 32768 tokens of 40
+// heads x 128 where three take 141 and two 167, and backward 161 where two
+// CTAs with two rows take 172.
+constexpr int kAhead = 4;
+
+template <typename T, bool VEC, int ROT, int LANES>
+__global__ void __launch_bounds__(kQkThreads, 4)
+    qk_norm_kernel(lq_qk_norm_config c, lq_qk_norm_args a, lq_qk_pair out, int any_lanes, int split) {
+    const int lanes = LANES > 0 ? LANES : any_lanes;
+    __shared__ __align__(16) float rows[ROT == ROT_SHARED ? kQkWarps * 32 * 8 : 4];
     const int64_t group = ((int64_t)blockIdx.x * kQkThreads + threadIdx.x) / lanes;
     Share s = share_of(c.d, lanes, split, group);
     const bool live = s.m < a.n_tokens;
     if (!live) s.m = a.n_tokens - 1, s.on = false;   // (the warp's shuffles want every lane)
     float *row = rows + (ROT == ROT_SHARED ? (threadIdx.x / lanes) * lanes * 8 : 0);
+    const float mean_of = c.norm == LQ_NORM_RMS ? 1.0f / (float)c.d : 1.0f;
     Turns<ROT> turns;
     turns.set(c, a, s.m, s.c0, s.lane);
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
         const bool is_q = which == 0;
         const int heads = is_q ? c.heads_q : c.heads_k;
-        const float scale = is_q ? c.q_scale : 1.0f;
         const int64_t x_head = is_q ? a.q_head : a.k_head, y_head = is_q ? out.q_head : out.k_head;
-        const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.c0;
-        T *y = static_cast<T *>(is_q ? out.q : out.k) + s.m * (is_q ? out.q_token : out.k_token) + s.c0;
-        float w[8];
-        load_weight(is_q ? a.weight_q : a.weight_k, s, w);
+        const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.part * x_head + s.c0;
+        T *y = static_cast<T *>(is_q ? out.q : out.k) + s.m * (is_q ? out.q_token : out.k_token) + s.part * y_head + s.c0;
+        const float *weight = is_q ? a.weight_q : a.weight_k;
+        float w[8], wp[8];
+        load_weight(weight, s, w);
+        load_partners<ROT>(c, weight, s, wp);
+        Linear<ROT> linear;
+        linear.template set<false>(turns, w, wp);
+        const float scale = is_q ? c.q_scale : 1.0f;
         for (int h0 = 0; h0 < heads; h0 += kAhead * split) {
             Raw8<T> raw[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int h = h0 + j * split + s.part;
                 zero8(raw[j]);
-                if (h < heads) load_row<T, VEC>(x + h * x_head, s, raw[j]);
+                if (h0 + j * split + s.part < heads) load_row<T, VEC>(x, s, raw[j]);
+                x += split * x_head;
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 if (h0 + j * split >= heads) break;      // (the same for every thread)
-                const int h = h0 + j * split + s.part;
-                float u[8];
+                float2 u[4], p[4], z[4];
                 widen8(raw[j], u);
-                const float r = scale_of(c, u, lanes);
+                const float r = scale * scale_of(c, row_dot(u, u, lanes), mean_of);
+                turns.partners(c, raw[j], u, row, s.c0, p);
+                linear.apply(u, p, z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] *= r * w[i];
-                turns.template turn<false>(c, row, s.c0, u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] *= scale;
-                if (h < heads && s.on) store8<VEC>(y + h * y_head, s.n, u);
+                for (int i = 0; i < 4; ++i) z[i] = mul2(make_float2(r, r), z[i]);
+                if (h0 + j * split + s.part < heads && s.on) store8<VEC>(y, s.n, z);
+                y += split * y_head;
             }
         }
     }
 }
 
-template <typename T, bool VEC, int ROT>
-__global__ void __launch_bounds__(kQkThreads)
+template <typename T, bool VEC, int ROT, int LANES>
+__global__ void __launch_bounds__(kQkThreads, 4)
     qk_norm_backward_kernel(lq_qk_norm_config c, lq_qk_norm_args a, lq_qk_pair gy, lq_qk_pair gx, float *partials,
-                            int lanes, int split, int64_t groups) {
-    __shared__ float rows[kQkThreads * 8];
+                            int any_lanes, int split, int64_t groups) {
+    const int lanes = LANES > 0 ? LANES : any_lanes;
+    __shared__ __align__(16) float rows[kQkThreads * 8];
     float *row = rows + (threadIdx.x / lanes) * lanes * 8;
     const int64_t first = ((int64_t)blockIdx.x * kQkThreads + threadIdx.x) / lanes;
     const int64_t all = (int64_t)gridDim.x * (kQkThreads / lanes);
     const int64_t rounds = (groups + all - 1) / all;
-    float dw[2][8] = {};                  // this thread's part of the weight gradients, q and k
+    const float mean_of = c.norm == LQ_NORM_RMS ? 1.0f / (float)c.d : 1.0f;
+    float2 dw[2][4] = {};                 // this thread's part of the weight gradients, q and k
     for (int64_t round = 0; round < rounds; ++round) {
         Share s = share_of(c.d, lanes, split, first + round * all);
         const bool live = s.m < a.n_tokens;
         if (!live) s.m = a.n_tokens - 1, s.on = false;
         Turns<ROT> turns;
         turns.set(c, a, s.m, s.c0, s.lane);
+        Linear<ROT> linear;
+        linear.template set<true>(turns, nullptr, nullptr);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const bool is_q = which == 0;
             const int heads = is_q ? c.heads_q : c.heads_k;
-            const float scale = is_q ? c.q_scale : 1.0f;
-            const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.c0;
-            const T *y = static_cast<const T *>(is_q ? gy.q : gy.k) + s.m * (is_q ? gy.q_token : gy.k_token) + s.c0;
-            T *z = static_cast<T *>(is_q ? gx.q : gx.k) + s.m * (is_q ? gx.q_token : gx.k_token) + s.c0;
             const int64_t x_head = is_q ? a.q_head : a.k_head, y_head = is_q ? gy.q_head : gy.k_head,
                           z_head = is_q ? gx.q_head : gx.k_head;
+            const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.part * x_head + s.c0;
+            const T *y = static_cast<const T *>(is_q ? gy.q : gy.k) + s.m * (is_q ? gy.q_token : gy.k_token) + s.part * y_head + s.c0;
+            T *z = static_cast<T *>(is_q ? gx.q : gx.k) + s.m * (is_q ? gx.q_token : gx.k_token) + s.part * z_head + s.c0;
             float w[8];
             load_weight(is_q ? a.weight_q : a.weight_k, s, w);
-            constexpr int AHEAD = 2;
-            for (int h0 = 0; h0 < heads; h0 += AHEAD * split) {
-                Raw8<T> rx[AHEAD], ry[AHEAD];
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    const int h = h0 + j * split + s.part;
-                    zero8(rx[j]);
-                    zero8(ry[j]);
+            const float scale = is_q ? c.q_scale : 1.0f;      // of the results: they are linear in dy
+            for (int h0 = 0; h0 < heads; h0 += split) {
+                const int h = h0 + s.part;
+                {
+                    Raw8<T> rx, ry;
+                    zero8(rx);
+                    zero8(ry);
                     if (h < heads) {
-                        load_row<T, VEC>(x + h * x_head, s, rx[j]);
-                        load_row<T, VEC>(y + h * y_head, s, ry[j]);
+                        load_row<T, VEC>(x, s, rx);
+                        load_row<T, VEC>(y, s, ry);
                     }
-                }
+                    float2 xh[4], dy[4], p[4], du[4];
+                    widen8(rx, xh);
+                    widen8(ry, dy);
+                    const float r = scale_of(c, row_dot(xh, xh, lanes), mean_of);
+                    turns.partners(c, ry, dy, row, s.c0, p);
+                    linear.apply(dy, p, du);                 // dz
 #pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    if (h0 + j * split >= heads) break;      // (the same for every thread)
-                    const int h = h0 + j * split + s.part;
-                    float xh[8], du[8], dot = 0.0f;
-                    widen8(rx[j], xh);
-                    widen8(ry[j], du);
-                    const float r = scale_of(c, xh, lanes);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) du[i] *= scale;
-                    turns.template turn<true>(c, row, s.c0, du);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        xh[i] *= r;
-                        dw[which][i] = fmaf(du[i], xh[i], dw[which][i]);
-                        du[i] *= w[i];
-                        dot = fmaf(xh[i], du[i], dot);
+                    for (int i = 0; i < 4; ++i) {
+                        xh[i] = mul2(make_float2(r, r), xh[i]);
+                        dw[which][i] = fma2(du[i], xh[i], dw[which][i]);
+                        du[i] = mul2(make_float2(w[2 * i], w[2 * i + 1]), du[i]);
                     }
-                    for (int o = lanes / 2; o > 0; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                    if (c.norm == LQ_NORM_RMS) dot /= (float)c.d;
+                    const float dot = -row_dot(xh, du, lanes) * mean_of, rs = r * scale;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) du[i] = r * fmaf(-xh[i], dot, du[i]);
-                    if (h < heads && s.on) store8<VEC>(z + h * z_head, s.n, du);
+                    for (int i = 0; i < 4; ++i) du[i] = mul2(make_float2(rs, rs), fma2(make_float2(dot, dot), xh[i], du[i]));
+                    if (h < heads && s.on) store8<VEC>(z, s.n, du);
                 }
+                x += split * x_head;
+                y += split * y_head;
+                z += split * z_head;
             }
         }
     }
@@ -268,12 +308,12 @@ __global__ void __launch_bounds__(kQkThreads)
     for (int k = 0; k < 2; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rows[threadIdx.x * 8 + i] = dw[k][i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(rows + threadIdx.x * 8 + 2 * i) = dw[k][i];
         __syncthreads();
         for (int e = threadIdx.x; e < c.d; e += kQkThreads) {
             float t = 0.0f;
             for (int i = 0; i < n_rows; ++i) t += rows[i * dp + e];
-            partials[((int64_t)k * gridDim.x + blockIdx.x) * c.d + e] = t;
+            partials[((int64_t)k * gridDim.x + blockIdx.x) * c.d + e] = k == 0 ? c.q_scale * t : t;
         }
     }
 }
@@ -294,17 +334,31 @@ __global__ void __launch_bounds__(1024) qk_weight_sum_kernel(const float *partia
     if (x == 0 && blockIdx.x * 32 + y < d) dst[blockIdx.x * 32 + y] = t;
 }
 
-template <typename T, bool VEC, int ROT>
+template <typename T, bool VEC, int ROT, int LANES_>
 struct Qk {
     using Type = T;
     static constexpr bool V = VEC;
-    static constexpr int R = ROT;
+    static constexpr int R = ROT, LANES = LANES_;    // LANES: of a row, where the kernel is compiled for them (0: any)
 };
+// Aligned rows are compiled for heads of 33..64, 65..128 and 129..256 channels:
+// the sums over a row then have no loop.
+template <typename T, bool VEC, int ROT, typename F>
+cudaError_t by_lanes(int d, F &&f) {
+    if constexpr (VEC) {
+        switch (row_lanes(d)) {
+            case 8: return f(Qk<T, VEC, ROT, 8>());
+            case 16: return f(Qk<T, VEC, ROT, 16>());
+            case 32: return f(Qk<T, VEC, ROT, 32>());
+            default: break;
+        }
+    }
+    return f(Qk<T, VEC, ROT, 0>());
+}
 template <typename T, bool VEC, typename F>
 cudaError_t by_rotation(const lq_qk_norm_config &c, F &&f) {
-    if (c.rot_dim == 0) return f(Qk<T, VEC, ROT_NONE>());
-    if (c.pairs == LQ_PAIRS_NEIGHBOURS) return f(Qk<T, VEC, ROT_NEIGHBOURS>());
-    return c.rot_dim % 16 == 0 ? f(Qk<T, VEC, ROT_SHUFFLE>()) : f(Qk<T, VEC, ROT_SHARED>());
+    if (c.rot_dim == 0) return by_lanes<T, VEC, ROT_NONE>(c.d, f);
+    if (c.pairs == LQ_PAIRS_NEIGHBOURS) return by_lanes<T, VEC, ROT_NEIGHBOURS>(c.d, f);
+    return c.rot_dim % 16 == 0 ? by_lanes<T, VEC, ROT_SHUFFLE>(c.d, f) : by_lanes<T, VEC, ROT_SHARED>(c.d, f);
 }
 template <typename F>
 cudaError_t by_kind(const lq_qk_norm_config &c, bool vec, F &&f) {
@@ -331,7 +385,7 @@ cudaError_t launch_qk_norm(const lq_qk_norm_config &c, const lq_qk_norm_args &a,
     const int lanes = row_lanes(c.d), split = split_of(c, a.n_tokens, lanes), rows = kQkThreads / lanes;
     return by_kind(c, vec, [&](auto k) {
         using K = decltype(k);
-        qk_norm_kernel<typename K::Type, K::V, K::R>
+        qk_norm_kernel<typename K::Type, K::V, K::R, K::LANES>
             <<<(unsigned)((a.n_tokens * split + rows - 1) / rows), kQkThreads, 0, s>>>(c, a, out, lanes, split);
         return cudaGetLastError();
     });
@@ -347,7 +401,7 @@ cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm
     if (grid > 0) {
         const cudaError_t e = by_kind(c, vec, [&](auto k) {
             using K = decltype(k);
-            qk_norm_backward_kernel<typename K::Type, K::V, K::R>
+            qk_norm_backward_kernel<typename K::Type, K::V, K::R, K::LANES>
                 <<<grid, kQkThreads, 0, s>>>(c, a, gy, gx, sums ? partials : nullptr, lanes, split, groups);
             return cudaGetLastError();
         });
