@@ -178,10 +178,10 @@ __device__ __forceinline__ float scale_of(const lq_qk_norm_config &c, float sum,
     return rsqrtf(fmaf(sum, mean_of, c.eps));
 }
 
-// Rows in flight per thread.  Threads count for more than registers here: four
-// CTAs an SM with four rows (one, backward) take 135 us for 32768 tokens of 40
-// heads x 128 where three take 141 and two 167, and backward 161 where two
-// CTAs with two rows take 172.
+// Rows in flight per thread, forward.  Threads count for more than registers
+// here: for 32768 tokens of 40 heads x 128 four CTAs an SM with four rows each
+// take 129 us, three 141 and two 167.  (Backward, 16384 tokens: three CTAs with
+// one row and its gradient 140 us, four 142, two 171.)
 constexpr int kAhead = 4;
 
 template <typename T, bool VEC, int ROT, int LANES>
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kQkThreads, 4)
 }
 
 template <typename T, bool VEC, int ROT, int LANES>
-__global__ void __launch_bounds__(kQkThreads, 4)
+__global__ void __launch_bounds__(kQkThreads, 3)
     qk_norm_backward_kernel(lq_qk_norm_config c, lq_qk_norm_args a, lq_qk_pair gy, lq_qk_pair gx, float *partials,
                             int any_lanes, int split, int64_t groups) {
     const int lanes = LANES > 0 ? LANES : any_lanes;
@@ -247,74 +247,68 @@ __global__ void __launch_bounds__(kQkThreads, 4)
     const int64_t all = (int64_t)gridDim.x * (kQkThreads / lanes);
     const int64_t rounds = (groups + all - 1) / all;
     const float mean_of = c.norm == LQ_NORM_RMS ? 1.0f / (float)c.d : 1.0f;
-    float2 dw[2][4] = {};                 // this thread's part of the weight gradients, q and k
+    // the CTAs of blockIdx.y = 0 take the queries and the others the keys: with
+    // both, the weight gradients' parts alone took 16 registers
+    const bool is_q = blockIdx.y == 0;
+    const int heads = is_q ? c.heads_q : c.heads_k;
+    const float scale = is_q ? c.q_scale : 1.0f;          // of the results: they are linear in dy
+    const int64_t x_head = is_q ? a.q_head : a.k_head, y_head = is_q ? gy.q_head : gy.k_head,
+                  z_head = is_q ? gx.q_head : gx.k_head;
+    float2 dw[4] = {};                    // this thread's part of the weight gradient
     for (int64_t round = 0; round < rounds; ++round) {
         Share s = share_of(c.d, lanes, split, first + round * all);
         const bool live = s.m < a.n_tokens;
         if (!live) s.m = a.n_tokens - 1, s.on = false;
+        Linear<ROT> linear;
         Turns<ROT> turns;
         turns.set(c, a, s.m, s.c0, s.lane);
-        Linear<ROT> linear;
         linear.template set<true>(turns, nullptr, nullptr);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const bool is_q = which == 0;
-            const int heads = is_q ? c.heads_q : c.heads_k;
-            const int64_t x_head = is_q ? a.q_head : a.k_head, y_head = is_q ? gy.q_head : gy.k_head,
-                          z_head = is_q ? gx.q_head : gx.k_head;
-            const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.part * x_head + s.c0;
-            const T *y = static_cast<const T *>(is_q ? gy.q : gy.k) + s.m * (is_q ? gy.q_token : gy.k_token) + s.part * y_head + s.c0;
-            T *z = static_cast<T *>(is_q ? gx.q : gx.k) + s.m * (is_q ? gx.q_token : gx.k_token) + s.part * z_head + s.c0;
-            float w[8];
-            load_weight(is_q ? a.weight_q : a.weight_k, s, w);
-            const float scale = is_q ? c.q_scale : 1.0f;      // of the results: they are linear in dy
-            for (int h0 = 0; h0 < heads; h0 += split) {
-                const int h = h0 + s.part;
-                {
-                    Raw8<T> rx, ry;
-                    zero8(rx);
-                    zero8(ry);
-                    if (h < heads) {
-                        load_row<T, VEC>(x, s, rx);
-                        load_row<T, VEC>(y, s, ry);
-                    }
-                    float2 xh[4], dy[4], p[4], du[4];
-                    widen8(rx, xh);
-                    widen8(ry, dy);
-                    const float r = scale_of(c, row_dot(xh, xh, lanes), mean_of);
-                    turns.partners(c, ry, dy, row, s.c0, p);
-                    linear.apply(dy, p, du);                 // dz
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        xh[i] = mul2(make_float2(r, r), xh[i]);
-                        dw[which][i] = fma2(du[i], xh[i], dw[which][i]);
-                        du[i] = mul2(make_float2(w[2 * i], w[2 * i + 1]), du[i]);
-                    }
-                    const float dot = -row_dot(xh, du, lanes) * mean_of, rs = r * scale;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) du[i] = mul2(make_float2(rs, rs), fma2(make_float2(dot, dot), xh[i], du[i]));
-                    if (h < heads && s.on) store8<VEC>(z, s.n, du);
-                }
-                x += split * x_head;
-                y += split * y_head;
-                z += split * z_head;
+        const T *x = static_cast<const T *>(is_q ? a.q : a.k) + s.m * (is_q ? a.q_token : a.k_token) + s.part * x_head + s.c0;
+        const T *y = static_cast<const T *>(is_q ? gy.q : gy.k) + s.m * (is_q ? gy.q_token : gy.k_token) + s.part * y_head + s.c0;
+        T *z = static_cast<T *>(is_q ? gx.q : gx.k) + s.m * (is_q ? gx.q_token : gx.k_token) + s.part * z_head + s.c0;
+        float w[8];
+        load_weight(is_q ? a.weight_q : a.weight_k, s, w);
+        for (int h0 = 0; h0 < heads; h0 += split) {
+            const bool mine = h0 + s.part < heads;
+            Raw8<T> rx, ry;
+            zero8(rx);
+            zero8(ry);
+            if (mine) {
+                load_row<T, VEC>(x, s, rx);
+                load_row<T, VEC>(y, s, ry);
             }
+            float2 xh[4], dy[4], p[4], du[4];
+            widen8(rx, xh);
+            widen8(ry, dy);
+            const float r = scale_of(c, row_dot(xh, xh, lanes), mean_of);
+            turns.partners(c, ry, dy, row, s.c0, p);
+            linear.apply(dy, p, du);                      // dz
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xh[i] = mul2(make_float2(r, r), xh[i]);
+                dw[i] = fma2(du[i], xh[i], dw[i]);
+                du[i] = mul2(make_float2(w[2 * i], w[2 * i + 1]), du[i]);
+            }
+            const float dot = -row_dot(xh, du, lanes) * mean_of, rs = r * scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) du[i] = mul2(make_float2(rs, rs), fma2(make_float2(dot, dot), xh[i], du[i]));
+            if (mine && s.on) store8<VEC>(z, s.n, du);
+            x += split * x_head;
+            y += split * y_head;
+            z += split * z_head;
         }
     }
     if (partials == nullptr) return;
     // the row groups' parts, channel by channel in a fixed order
     const int dp = lanes * 8, n_rows = kQkThreads / lanes;
+    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(rows + threadIdx.x * 8 + 2 * i) = dw[k][i];
-        __syncthreads();
-        for (int e = threadIdx.x; e < c.d; e += kQkThreads) {
-            float t = 0.0f;
-            for (int i = 0; i < n_rows; ++i) t += rows[i * dp + e];
-            partials[((int64_t)k * gridDim.x + blockIdx.x) * c.d + e] = k == 0 ? c.q_scale * t : t;
-        }
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(rows + threadIdx.x * 8 + 2 * i) = dw[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < c.d; e += kQkThreads) {
+        float t = 0.0f;
+        for (int i = 0; i < n_rows; ++i) t += rows[i * dp + e];
+        partials[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * c.d + e] = scale * t;
     }
 }
 
@@ -402,7 +396,8 @@ cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm
         const cudaError_t e = by_kind(c, vec, [&](auto k) {
             using K = decltype(k);
             qk_norm_backward_kernel<typename K::Type, K::V, K::R, K::LANES>
-                <<<grid, kQkThreads, 0, s>>>(c, a, gy, gx, sums ? partials : nullptr, lanes, split, groups);
+                <<<dim3(grid, c.heads_k > 0 ? 2 : 1), kQkThreads, 0, s>>>(c, a, gy, gx, sums ? partials : nullptr, lanes, split,
+                                                                         groups);
             return cudaGetLastError();
         });
         if (e != cudaSuccess) return e;
