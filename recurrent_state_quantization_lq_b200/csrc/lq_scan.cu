@@ -471,20 +471,32 @@ __global__ void __launch_bounds__(kRowsThreads) scan_rows_kernel(lq_scan_args a,
         load8<VEC>(a.h0 + state, n, r);
         widen8(r, h);
     }
-    for (int t = 0; t < w.len; ++t) {
-        Raw8<InT> raw;
-        load8<VEC>(static_cast<const InT *>(a.v) + row_of(a.v_stride, w, t) + c0, n, raw);
-        Gates<CHAN> gate;
-        gate.template load<VEC>(a.g + row_of(a.g_stride, w, t) + (CHAN ? c0 : 0), n);
-        const float beta = a.beta != nullptr ? __ldg(a.beta + row_of(a.beta_stride, w, t)) : 1.0f;
-        if (a.checkpoints != nullptr && t % every == 0)
-            store8<VEC>(a.checkpoints + (int64_t)(t / every) * units * d + state, n, h);
-        gate.exponentiate();
-        float2 v[4];
-        widen8(raw, v);
+    constexpr int AHEAD = 4;         // tokens in flight
+    for (int t0 = 0; t0 < w.len; t0 += AHEAD) {
+        Raw8<InT> raw[AHEAD];
+        Gates<CHAN> gate[AHEAD];
+        float beta[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fma2(gate[i], h[i], mul2(make_float2(beta, beta), v[i]));
-        if (a.out != nullptr) store8<VEC>(static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t) + c0, n, h);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int t = t0 + i;
+            if (t >= w.len) break;
+            load8<VEC>(static_cast<const InT *>(a.v) + row_of(a.v_stride, w, t) + c0, n, raw[i]);
+            gate[i].template load<VEC>(a.g + row_of(a.g_stride, w, t) + (CHAN ? c0 : 0), n);
+            beta[i] = a.beta != nullptr ? __ldg(a.beta + row_of(a.beta_stride, w, t)) : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int t = t0 + i;
+            if (t >= w.len) break;
+            if (a.checkpoints != nullptr && t % every == 0)
+                store8<VEC>(a.checkpoints + (int64_t)(t / every) * units * d + state, n, h);
+            gate[i].exponentiate();
+            float2 v[4];
+            widen8(raw[i], v);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[c] = fma2(gate[i][c], h[c], mul2(make_float2(beta[i], beta[i]), v[c]));
+            if (a.out != nullptr) store8<VEC>(static_cast<OutT *>(a.out) + row_of(a.out_stride, w, t) + c0, n, h);
+        }
     }
     if (a.h_last != nullptr) store8<VEC>(a.h_last + state, n, h);
     if (a.zero_past && a.out != nullptr) {
@@ -1214,6 +1226,7 @@ cudaError_t row_map(RowMap *m, const void *p, const lq_strides &s, const lq_scan
 // the most that any d wants (for the kernel's limit).
 struct Plan {
     int ranks, smem, most, chunk;
+    long long rounds;        // of CTAs on the device
 };
 
 // As many CTAs as take the least time: rounds of CTAs on the device, each its
@@ -1224,7 +1237,7 @@ struct Plan {
 template <typename S>
 Plan plan_of(int units, long long tokens, int d, int run, int most_ctas, int shared) {
     auto space = [run](int dd) { return S(dd, row_lanes(dd), run); };
-    Plan p{1, 0, 0, space(d).tokens};
+    Plan p{1, 0, 0, space(d).tokens, 1};
     long long least = -1;
     for (int r = 1; r <= kMostRanks; ++r) {
         const int smem = space(d).bytes(r);
@@ -1235,6 +1248,7 @@ Plan plan_of(int units, long long tokens, int d, int run, int most_ctas, int sha
             least = cost;
             p.ranks = r;
             p.smem = smem;
+            p.rounds = rounds;
         }
     }
     for (int dd = 8; dd <= 256; dd *= 2) p.most = std::max(p.most, space(dd).bytes(kMostRanks));
@@ -1248,15 +1262,19 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
     return by_variant(c, vec, [&](auto k) {
         using K = decltype(k);
         using In = typename K::In;
-        if (a.n_tokens <= 4) {
+        constexpr int run = forward_run(sizeof(In) == 2, K::CHAN);
+        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run, 2, 115);
+        // Token after token takes 6 us and 0.35 us a token while the threads fit the
+        // device; the split kernel 4 us and 4.4 us a round of CTAs while a CTA has
+        // one step.  (2048 units of 128 channels, 16 tokens: 12 against 31 us; 32
+        // units: 10 against 8.)
+        if (a.n_tokens <= std::min(12 * p.rounds - 6, 64LL)) {
             const long long threads = (long long)units * lanes;
             scan_rows_kernel<In, typename K::Out, K::CHAN, K::VEC>
                 <<<(unsigned)((threads + kRowsThreads - 1) / kRowsThreads), kRowsThreads, 0, s>>>(a, c.heads, units, c.d,
                                                                                                  lanes, every);
             return cudaGetLastError();
         }
-        constexpr int run = forward_run(sizeof(In) == 2, K::CHAN);
-        const Plan p = plan_of<ForwardSpace<In, K::CHAN>>(units, a.n_tokens, c.d, run, 2, 115);
         RowMap v = {}, g = {};
         if (K::VEC) {
             cudaError_t e = row_map(&v, a.v, a.v_stride, c, a.n_tokens, c.in_dtype, p.chunk);
