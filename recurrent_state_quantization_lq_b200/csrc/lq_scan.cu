@@ -46,7 +46,7 @@ namespace lq {
 // Warps that run tokens, beside the composer and the loader.  Forward, three
 // stages of tokens and two steps' maps of two CTAs just fit an SM's shared
 // memory; backward, two CTAs of eight warps leave a thread 128 registers.
-constexpr int kForwardWarps = 7;
+constexpr int forward_warps(bool chan) { return chan ? 6 : 7; }
 constexpr int kBackwardWarps = 6;
 constexpr int kStages = 3;                       // steps whose tokens are in shared memory
 constexpr int kMostRanks = 8;                    // CTAs of a cluster (the portable size)
@@ -54,7 +54,7 @@ constexpr int kRowsThreads = 256;                // of the kernel for a few toke
 
 // Consecutive tokens that a row of lanes takes in a step: as many as the two
 // CTAs' stages have room for.
-constexpr int forward_run(bool bf16, bool chan) { return chan ? 2 : bf16 ? 8 : 4; }
+constexpr int forward_run(bool bf16, bool chan) { return chan ? (bf16 ? 3 : 2) : bf16 ? 8 : 4; }
 constexpr int backward_run(bool bf16, bool chan) { return bf16 && !chan ? 4 : 2; }
 
 // (a multiple of every forward_run of the same types, so that a checkpoint
@@ -507,15 +507,15 @@ __global__ void __launch_bounds__(kRowsThreads) scan_rows_kernel(lq_scan_args a,
 }
 
 template <typename InT, bool CHAN>
-using ForwardSpace = Space<kForwardWarps, (int)sizeof(InT), CHAN ? 4 : 0, 0, CHAN, false>;
+using ForwardSpace = Space<forward_warps(CHAN), (int)sizeof(InT), CHAN ? 4 : 0, 0, CHAN, false>;
 
 template <typename InT, typename OutT, bool CHAN, bool VEC, int D_>
-__global__ void __launch_bounds__(32 * kForwardWarps + 64, 2)
+__global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
     scan_forward_kernel(lq_scan_args a, const __grid_constant__ RowMap map_v, const __grid_constant__ RowMap map_g,
                         int heads, int units, int any_d, int every) {
     const int d = D_ > 0 ? D_ : any_d, lanes = row_lanes(d);
     constexpr int R = forward_run(sizeof(InT) == 2, CHAN);
-    constexpr int NW = kForwardWarps;
+    constexpr int NW = forward_warps(CHAN);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Bars bars;
     const int rows = 32 * NW / lanes, chunk = rows * R;
@@ -1282,7 +1282,7 @@ cudaError_t launch_scan_forward(const lq_scan_config &c, const lq_scan_args &a, 
             if (e != cudaSuccess) return e;
         }
         return launch_clusters<scan_forward_kernel<In, typename K::Out, K::CHAN, K::VEC, K::D>>(
-            32 * kForwardWarps + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, every);
+            32 * forward_warps(K::CHAN) + 64, units, p.ranks, p.smem, p.most, s, a, v, g, c.heads, units, c.d, every);
     });
 }
 
