@@ -47,7 +47,28 @@ struct Turns {
     __device__ __forceinline__ void set(const lq_qk_norm_config &c, const lq_qk_norm_args &a, int64_t m, int c0, int lane) {
         if constexpr (ROT != ROT_NONE) {
             const int pos = __ldg(a.positions + m), half = c.rot_dim / 2;
-            if (ROT == ROT_SHUFFLE) partner = c0 >= c.rot_dim ? lane : c0 < half ? lane + half / 8 : lane - half / 8;
+            if constexpr (ROT == ROT_SHUFFLE) {
+                // the partners have the same eight angles: each forms four
+                const bool any = c0 < c.rot_dim, second = c0 >= half;
+                partner = !any ? lane : second ? lane - half / 8 : lane + half / 8;
+                const int k = second ? c0 - half + 4 : c0;
+                float ca[4], sa[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ca[i] = 1.0f;
+                    sa[i] = 0.0f;
+                    if (any) angle_of(pos, __ldg(a.inv_freq + k + i), &ca[i], &sa[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float co = __shfl_sync(0xffffffffu, ca[i], partner), so = __shfl_sync(0xffffffffu, sa[i], partner);
+                    cs[i] = second ? co : ca[i];
+                    cs[i + 4] = second ? ca[i] : co;
+                    sn[i] = second ? so : -sa[i];
+                    sn[i + 4] = second ? sa[i] : -so;
+                }
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int e = c0 + i;
@@ -180,8 +201,8 @@ __device__ __forceinline__ float scale_of(const lq_qk_norm_config &c, float sum,
 
 // Rows in flight per thread, forward.  Threads count for more than registers
 // here: for 32768 tokens of 40 heads x 128 four CTAs an SM with four rows each
-// take 129 us, three 141 and two 167.  (Backward, 16384 tokens: three CTAs with
-// one row and its gradient 140 us, four 142, two 171.)
+// take 129 us, three 141 and two 167.  (Backward, 16384 tokens: three CTAs
+// with a row and its gradient ahead 128 us, four 159, two 143.)
 constexpr int kAhead = 4;
 
 template <typename T, bool VEC, int ROT, int LANES>
@@ -268,15 +289,22 @@ __global__ void __launch_bounds__(kQkThreads, 3)
         T *z = static_cast<T *>(is_q ? gx.q : gx.k) + s.m * (is_q ? gx.q_token : gx.k_token) + s.part * z_head + s.c0;
         float w[8];
         load_weight(is_q ? a.weight_q : a.weight_k, s, w);
+        Raw8<T> next_x, next_y;                           // a row ahead
+        auto fetch = [&](int h0) {
+            zero8(next_x);
+            zero8(next_y);
+            if (h0 + s.part < heads) {
+                load_row<T, VEC>(x, s, next_x);
+                load_row<T, VEC>(y, s, next_y);
+            }
+            x += split * x_head;
+            y += split * y_head;
+        };
+        fetch(0);
         for (int h0 = 0; h0 < heads; h0 += split) {
             const bool mine = h0 + s.part < heads;
-            Raw8<T> rx, ry;
-            zero8(rx);
-            zero8(ry);
-            if (mine) {
-                load_row<T, VEC>(x, s, rx);
-                load_row<T, VEC>(y, s, ry);
-            }
+            const Raw8<T> rx = next_x, ry = next_y;
+            fetch(h0 + split);
             float2 xh[4], dy[4], p[4], du[4];
             widen8(rx, xh);
             widen8(ry, dy);
@@ -293,8 +321,6 @@ __global__ void __launch_bounds__(kQkThreads, 3)
 #pragma unroll
             for (int i = 0; i < 4; ++i) du[i] = mul2(make_float2(rs, rs), fma2(make_float2(dot, dot), xh[i], du[i]));
             if (mine && s.on) store8<VEC>(z, s.n, du);
-            x += split * x_head;
-            y += split * y_head;
             z += split * z_head;
         }
     }
