@@ -437,7 +437,7 @@ typedef struct lq_scan_config {
 } lq_scan_config;
 
 typedef struct lq_scan_args {
-    int32_t n_tokens;          /* T, >= 0                                         */
+    int32_t n_tokens;          /* T, 0..2^30                                      */
     int32_t zero_past;         /* rows of the outputs and of the gradients of v, g
                                   and beta past a length: 0 left as they are,
                                   1 set to zero                                   */
@@ -470,8 +470,8 @@ typedef struct lq_scan_grads {
     lq_strides grad_out_stride, grad_v_stride, grad_g_stride, grad_beta_stride;
 } lq_scan_grads;
 
-/* Bytes of the checkpoints of n_tokens tokens (0 for an invalid config or a
- * negative count).  Source: none (memory sizing). */
+/* Bytes of the checkpoints of n_tokens tokens (0 for an invalid config or
+ * count).  Source: none (memory sizing). */
 LQ_API size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t n_tokens);
 
 /*
@@ -480,7 +480,7 @@ LQ_API size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t 
  * the device.  With `checkpoints` it leaves there what the backward pass needs
  * besides the inputs.
  * Errors: LQ_ERR_INVALID_ARG for a bad config field, a NULL v or g with
- * n_tokens > 0, a negative n_tokens, a pointer not aligned to its element or
+ * n_tokens > 0, an n_tokens out of range, a pointer not aligned to its element or
  * an output dimension of stride 0.
  * Source: [abs] (the gated linear recurrence that GDN and KDA build on; the
  * pages describe no vector-state layer).
@@ -569,7 +569,8 @@ LQ_API size_t lq_qk_norm_rotate_workspace_bytes(const lq_qk_norm_config *cfg);
  * The gradients of lq_qk_norm_rotate(): `args` as in the forward call (q and k
  * the original inputs), `grad_out` the gradients of its outputs (read only),
  * `grad_in` those of q and k (may be grad_out itself: in place), grad_weight_q
- * and grad_weight_k f32 [d] (NULL: not wanted; only where the weight is given).
+ * and grad_weight_k f32 [d] (NULL: not wanted; only where the weight, and for
+ * grad_weight_k any keys, are given).
  * workspace: lq_qk_norm_rotate_workspace_bytes() bytes, 16-byte aligned; needed
  * only with a weight gradient.  Errors: as lq_qk_norm_rotate(), and
  * LQ_ERR_WORKSPACE for a missing or misaligned workspace.

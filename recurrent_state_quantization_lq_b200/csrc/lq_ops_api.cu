@@ -51,6 +51,7 @@ bool strides_cover(const void *p, const lq_strides &s, int64_t T, int64_t B, int
 const char *why_not(const lq_scan_config &c, const lq_scan_args *a, bool *vec) {
     if (a == nullptr) return "args is NULL";
     if (a->n_tokens < 0) return "negative n_tokens";
+    if (a->n_tokens > (1 << 30)) return "n_tokens must be <= 2^30";
     if (a->zero_past != 0 && a->zero_past != 1) return "zero_past must be 0 or 1";
     if (a->n_tokens > 0 && (a->v == nullptr || a->g == nullptr)) return "NULL v or g";
     if (!aligned(a->v, element(c.in_dtype)) || !aligned(a->out, element(c.out_dtype)) || !aligned(a->g, 4) ||
@@ -119,7 +120,7 @@ extern "C" {
 
 size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t n_tokens) {
     const char *why = why_not(cfg);
-    if (why == nullptr && n_tokens < 0) why = "negative n_tokens";
+    if (why == nullptr && (n_tokens < 0 || n_tokens > (1 << 30))) why = "n_tokens must be in 0..2^30";
     if (why != nullptr) {
         fail(LQ_ERR_INVALID_ARG, why);
         return 0;
@@ -197,6 +198,7 @@ lq_status lq_qk_norm_rotate_backward(const lq_qk_norm_config *cfg, const lq_qk_n
     if (const char *why = why_not(*cfg, args->n_tokens, grad_in, true)) return fail(LQ_ERR_INVALID_ARG, why);
     if ((grad_weight_q != nullptr && args->weight_q == nullptr) || (grad_weight_k != nullptr && args->weight_k == nullptr))
         return fail(LQ_ERR_INVALID_ARG, "a weight gradient without its weight");
+    if (grad_weight_k != nullptr && cfg->heads_k == 0) return fail(LQ_ERR_INVALID_ARG, "a weight gradient of keys without keys");
     if (!aligned(grad_weight_q, 4) || !aligned(grad_weight_k, 4))
         return fail(LQ_ERR_INVALID_ARG, "a pointer is not aligned to its element");
     if ((grad_weight_q != nullptr || grad_weight_k != nullptr) && (workspace == nullptr || !aligned(workspace, 16)))

@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
     const float *pg = a.g + row_of(a.g_stride, w, 0);
     const float *pb = a.beta != nullptr ? a.beta + row_of(a.beta_stride, w, 0) : nullptr;
 
+    float4 last[2];                        // the composer's: the last state
     if (warp == NW + 1) {                  // the loader
         Turn turn;
         for (int s = 0; s < steps; ++s, turn.next()) {
@@ -572,11 +573,8 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
             composer.run(s, H, H + NW * dp);
         }
         meet<1, 32 * NW + 32>();
-        if (rank == 0 && a.h_last != nullptr)
-            for (int j = 0; j < 2; ++j) {
-                const int c = 4 * (lane + 32 * j);
-                store4(a.h_last + state + c, d - c, composer.carry[j]);
-            }
+        last[0] = composer.carry[0];
+        last[1] = composer.carry[1];
     } else {                                         // the workers
         const int in_row = lane & (lanes - 1), c0 = in_row * 8, row = tid / lanes;
         const bool on = c0 < d;
@@ -714,6 +712,13 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
     }
     __syncthreads();
     if (ranks > 1) cluster.sync();                   // no CTA leaves while another may still store to it
+    // only now: h_last may be h0, which every CTA of the cluster reads
+    if (warp == NW && rank == 0 && a.h_last != nullptr)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = 4 * (lane + 32 * j);
+            store4(a.h_last + (int64_t)w.u * d + c, d - c, last[j]);
+        }
 }
 
 // ------------------------------------------------------------------ backward
@@ -785,6 +790,12 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
     const float *pg = a.g + row_of(a.g_stride, w, 0);
     const float *pb = a.beta != nullptr ? a.beta + row_of(a.beta_stride, w, 0) : nullptr;
 
+    // A worker composes channel tid (and tid + 32 NW where there are as many);
+    // where half of the threads are enough for the states, the other half
+    // composes the gradients.
+    constexpr int NC = D_ > 0 && D_ <= 32 * NW ? 1 : 2;
+    const int e_from = dp <= 16 * NW ? 16 * NW : 0;
+    float carry[NC];                 // what enters a step from behind
     if (warp == NW) {                                // the loader
         const int v_bytes = d * (int)sizeof(InT), y_bytes = py != nullptr ? d * (int)sizeof(OutT) : 0;
         auto live_of = [&](int s) { return min(max(w.len - first_of(s), 0), chunk); };
@@ -875,12 +886,6 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
         const int64_t gv_step = stride * g.grad_v_stride.token, gg_step = stride * g.grad_g_stride.token,
                       sum_step = stride * sum_stride.token;
 
-        // A thread composes channel tid (and tid + 32 NW where there are as many);
-        // where half of the threads are enough for the states, the other half
-        // composes the gradients.
-        constexpr int NC = D_ > 0 && D_ <= 32 * NW ? 1 : 2;
-        const int e_from = dp <= 16 * NW ? 16 * NW : 0;
-        float carry[NC];             // what enters a step from behind
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             const int c = tid - e_from + 32 * NW * j;
@@ -1116,12 +1121,6 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
             if (!VEC) bring(s + kStages, turn.stage);
             turn.next();
         }
-        if (rank == 0 && g.grad_h0 != nullptr)
-#pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int c = tid - e_from + 32 * NW * j;
-                if (c >= 0 && c < d) g.grad_h0[(int64_t)w.u * d + c] = carry[j];
-            }
         if (a.zero_past && on) {
             const float2 zero[4] = {};
 #pragma unroll 1
@@ -1135,6 +1134,13 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
     }
     __syncthreads();
     if (ranks > 1) cluster.sync();                   // no CTA leaves while another may still store to it
+    // only now: grad_h0 may be grad_last, which every CTA of the cluster reads
+    if (warp < NW && rank == 0 && g.grad_h0 != nullptr)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int c = tid - e_from + 32 * NW * j;
+            if (c >= 0 && c < d) g.grad_h0[(int64_t)w.u * d + c] = carry[j];
+        }
 }
 
 // ------------------------------------------------------------------ dispatch

@@ -440,7 +440,7 @@ def qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k=None, *, positions=None
     """The gradients of qk_norm_rotate() (lq_qk_norm_rotate_backward): q, k and
     the keywords as in the forward call, grad_q_out and grad_k_out those of
     its results.  Returns (grad_q, grad_k, grad_weight_q, grad_weight_k), the
-    last two FP32 [d], None where there is no weight."""
+    last two FP32 [d], None where there is no weight (or are no keys)."""
     on = _on(q, stream)
     if on is not None:
         with on:
@@ -453,7 +453,7 @@ def qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k=None, *, positions=None
     if k is not None and grad_k is None:
         grad_k = k.new_empty(k.shape)
     gwq = None if weight_q is None else torch.empty_like(weight_q)
-    gwk = None if weight_k is None else torch.empty_like(weight_k)
+    gwk = None if weight_k is None or k is None else torch.empty_like(weight_k)
     work = None
     if gwq is not None or gwk is not None:
         n = lib().lq_qk_norm_rotate_workspace_bytes(cfg)

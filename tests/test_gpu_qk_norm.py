@@ -114,6 +114,13 @@ def test_queries_alone_and_leading_dimensions():
         lq.qk_norm_rotate(q4.transpose(0, 1), **{**how, "positions": pos.t().contiguous()})
 
 
+def test_a_key_weight_without_keys():
+    c, how = case(20, 3, 1, 64, seed=12)
+    want = lq.qk_norm_rotate_backward(c["gq"], c["gk"], c["q"], c["k"], **how)
+    gq, none, gwq, gwk = lq.qk_norm_rotate_backward(c["gq"], None, c["q"], **how)
+    assert none is None and gwk is None and torch.equal(gq, want[0]) and torch.equal(gwq, want[2])
+
+
 def test_in_place_backward():
     c, how = case(30, 3, 2, 128, rot=128, seed=7)
     want = lq.qk_norm_rotate_backward(c["gq"], c["gk"], c["q"], c["k"], **how)

@@ -174,6 +174,46 @@ def test_state_in_place_and_tokens_one_by_one():
     plain_ops.check(h, want["h_last"], F32, "h_last")
 
 
+@pytest.mark.parametrize("T", [40, 900, 5000])
+def test_state_and_gradient_in_place_over_a_cluster(T):
+    """h_last may be h0 and grad_h0 grad_last also where several CTAs read them."""
+    c = case(T, 1, 2, 128, seed=T)
+    want = run(c)
+    for _ in range(5):
+        h, dh = c["h0"].clone(), c["grad_last"].clone()
+        marks = lq.gated_scan_checkpoints(c["v"], c["g"])
+        out, last = lq.gated_scan(c["v"], c["g"], c["beta"], h, h_last=h, checkpoints=marks)
+        gh = lq.gated_scan_backward(c["grad_out"], c["v"], c["g"], c["beta"], checkpoints=marks, grad_last=dh,
+                                    grad_h0=dh)[3]
+        assert last is h and gh is dh and torch.equal(out, want["out"])
+        assert torch.equal(h, want["h_last"]) and torch.equal(dh, want["grad_h0"])
+
+
+@pytest.mark.parametrize("T", [6, 18, 40, 64, 65])
+def test_few_tokens_of_many_heads(T):
+    """On both sides of the token-by-token kernel's rule, with its checkpoints."""
+    c = case(T, 40, 32, 64, seed=T, ragged=True)
+    verify(c, run(c))
+
+
+def test_two_calls_at_once():
+    """Two streams run the same operator on their own data."""
+    cs = [case(3000, 2, 8, 128, seed=s) for s in (1, 2)]
+    want = [run(c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = [[], []]
+    for _ in range(4):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(run(c))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for n in r:
+                assert torch.equal(r[n], want[i][n]), n
+
+
 def test_a_split_prompt_continues():
     c = case(900, 2, 2, 64, seed=6)
     whole, last = lq.gated_scan(c["v"], c["g"], c["beta"], c["h0"], out_dtype=F32)

@@ -40,7 +40,7 @@ def test_scan_configs_refused(field, value):
     assert L.lq_gated_scan_backward(ref(cfg), ref(scan_args()), ref(scan_grads()), None) == lq.LQ_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw,word", [({"n_tokens": -1}, "negative"), ({"zero_past": 2}, "zero_past"), ({"v": None}, "NULL"),
+@pytest.mark.parametrize("kw,word", [({"n_tokens": -1}, "negative"), ({"n_tokens": (1 << 30) + 1}, "2^30"), ({"zero_past": 2}, "zero_past"), ({"v": None}, "NULL"),
                                      ({"g": None}, "NULL"), ({"v": P + 1}, "aligned"), ({"g": P + 2}, "aligned"),
                                      ({"lengths": P + 1}, "aligned"), ({"h0": P + 2}, "aligned"),
                                      ({"checkpoints": P + 3}, "aligned"), ({"beta": P + 1}, "aligned")])
@@ -125,6 +125,8 @@ def test_qk_outputs_and_workspaces_refused():
     assert back(ref(cfg), ref(qk_args()), ref(pair()), ref(pair()), P, P, P + 4, None) == lq.LQ_ERR_WORKSPACE
     assert back(ref(cfg), ref(qk_args(weight_q=None)), ref(pair()), ref(pair()), P, None, P, None) == lq.LQ_ERR_INVALID_ARG
     assert back(ref(cfg), ref(qk_args()), None, ref(pair()), None, None, None, None) == lq.LQ_ERR_INVALID_ARG
+    none = qk_config(heads_k=0)                        # a key weight may be there, its gradient may not
+    assert back(ref(none), ref(qk_args()), ref(pair()), ref(pair()), P, P, P, None) == lq.LQ_ERR_INVALID_ARG
     assert L.lq_qk_norm_rotate(ref(cfg), ref(qk_args()), None, None) == lq.LQ_ERR_INVALID_ARG
 
 
