@@ -303,6 +303,11 @@ __device__ __forceinline__ void init_bars(Bars &b, int workers) {
     fence_mbar_init();
 }
 
+// Every wait is bounded.  After one that ran out, what follows is NaN (tokens or
+// a peer's map never came) and the later waits, for the copies still on their
+// way, are short.
+__device__ __forceinline__ long long budget_of(bool alive) { return alive ? kWaitBudgetCycles : 200000LL; }
+
 // The stage of a step and the parity of its use, counted without divisions.
 struct Turn {
     int stage = 0, parity = 0;
@@ -333,7 +338,7 @@ __device__ __forceinline__ void peer_store(uint32_t dst, float4 x, uint32_t bar)
                  "r"(__float_as_uint(x.w)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ bool peer_wait(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool peer_wait(uint64_t *bar, uint32_t parity, long long budget_cycles) {
     const long long t0 = clock64();
     while (true) {
         uint32_t ok;
@@ -345,7 +350,7 @@ __device__ __forceinline__ bool peer_wait(uint64_t *bar, uint32_t parity) {
             : "r"(smem_u32(bar)), "r"(parity)
             : "memory");
         if (ok) return true;
-        if (clock64() - t0 > kWaitBudgetCycles) return false;
+        if (clock64() - t0 > budget_cycles) return false;
     }
 }
 
@@ -384,7 +389,7 @@ struct Composer {
     uint64_t *bars;          // [2]
     int ranks, rank, dp;
     float4 carry[2];         // the state before the step
-    bool alive = true;       // a wait that ran out is the last one, and what follows it is NaN
+    bool alive = true;       // until a wait runs out
 
     __device__ __forceinline__ int owned() const { return (dp / 4 - (int)(threadIdx.x % 32) + 31) / 32; }
     __device__ __forceinline__ Map4 map(const float *H, const float *A, int k, int q) const {
@@ -416,7 +421,7 @@ struct Composer {
                     if (CHAN || q == 0) peer_store(dst + (dp + 4 * q) * 4, all.A, b);
                 }
             }
-            if (alive) alive = peer_wait(bars + p, (step >> 1) & 1);
+            alive = peer_wait(bars + p, (step >> 1) & 1, budget_of(alive)) && alive;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -588,7 +593,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
         };
         if (!VEC)
             for (int s = 0; s < kStages; ++s) bring(s, s);
-        bool alive = true;           // a wait that ran out is the last one, and what follows it is NaN
+        bool alive = true;           // until a wait runs out
         Turn one, two;               // the stages of pass one and pass two
         // the row's first token is past_mark tokens past checkpoint `mark`, step after step
         const int stride_marks = stride / every, stride_past = stride - stride_marks * every;
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
                 unsigned char *base = smem + one.stage * space.stage();
                 float2 *sc = reinterpret_cast<float2 *>(base + space.scalars()) + row * R;
                 float *sH = maps + (s & 1) * space.map(), *sA = sH + NW * dp;
-                if (alive) alive = mbar_wait(&bars.full[one.stage], one.parity, kWaitBudgetCycles);
+                alive = mbar_wait(&bars.full[one.stage], one.parity, budget_of(alive)) && alive;
                 if (!alive) A.fill(nanf(""));
                 // each gate is raised once, by one lane of its row; past the end it is 1, and beta 0
                 for (int i = in_row; i < R; i += lanes) {
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
             const int c = tid - e_from + 32 * NW * j;
             carry[j] = c >= 0 && c < d && g.grad_last != nullptr ? g.grad_last[(int64_t)w.u * d + c] : 0.0f;
         }
-        bool alive = true;           // a wait that ran out is the last one, and what follows it is NaN
+        bool alive = true;           // until a wait runs out
         Turn turn;
         for (int s = 0; s < steps; ++s) {
             const int t_row = first_of(s) + row * R, live = min(max(w.len - t_row, 0), R);
@@ -901,7 +906,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
             float2 ah[R][4], D[R][4], H[4] = {}, E[4] = {};
             A.fill(1.0f);
             B.fill(1.0f);
-            if (alive) alive = mbar_wait(&bars.full[turn.stage], turn.parity, kWaitBudgetCycles);
+            alive = mbar_wait(&bars.full[turn.stage], turn.parity, budget_of(alive)) && alive;
             if (!alive) A.fill(nanf(""));
             if (live < R && on) {                    // what lies past the sequence's end is nothing
 #pragma unroll 1
@@ -1027,7 +1032,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
                 const float *Ac = A_last + (CHAN ? c : 0);
                 float x = carry[j];
                 if (ranks > 1) {
-                    if (alive) alive = peer_wait(bars.peer + p, (s >> 1) & 1);
+                    alive = peer_wait(bars.peer + p, (s >> 1) & 1, budget_of(alive)) && alive;
                     if (!alive) carry[j] = nanf("");
 #pragma unroll 1
                     for (int r = ranks - 1; r >= 0; --r) {
