@@ -521,11 +521,15 @@ class DecodeState:
         self._check(lib().lq_prefill_state(self._h, _ptr(S0), _stream_ptr(stream, self.device)),
                     "lq_prefill_state")
 
-    def _normed(self, q, k, positions, stream):
+    def _normed(self, q, k, positions, stream, n_tokens: int = 1):
         """q and k as the C ABI takes them: through qk_norm where the state has one."""
         if self.qk_norm is None:
             assert positions is None, "positions without qk_norm"
             return q, k
+        for x in (q, k):            # the norm takes any number of heads, the state its own
+            assert x is not None and x.shape[-2:] == (self.heads, self.d) and \
+                x.numel() == n_tokens * self.batch * self.heads * self.d, \
+                f"q and k are [batch, heads, d], for a prompt [T, batch, heads, d]: {None if x is None else tuple(x.shape)}"
         return qk_norm_rotate(q, k, positions=positions, stream=stream, **self.qk_norm)
 
     def decode_step(self, q, k, v, g, beta, out: torch.Tensor | None = None, stream=None,
@@ -573,7 +577,7 @@ class DecodeState:
         as for decode_step, stacked over tokens) from S0 (None = zero state) and
         encode its final state as the window-start state.  Writes the prompt's
         outputs into `out` ([T, batch, heads, d] FP32) when given."""
-        q, k = self._normed(q, k, positions, stream)
+        q, k = self._normed(q, k, positions, stream, v.shape[0])
         T = q.shape[0]
         for t, dt in ((q, self.in_dtype), (k, self.in_dtype), (v, self.in_dtype), (g, torch.float32),
                       (beta, torch.float32)):
@@ -594,7 +598,7 @@ class DecodeState:
         """Ragged: restart the sequences with mask[b] != 0 from S0 (None = zero)
         through their prompts: inputs [T, batch, heads, ...] padded to T tokens,
         lengths int32 [batch] on the device (None = T for every sequence)."""
-        q, k = self._normed(q, k, positions, stream)
+        q, k = self._normed(q, k, positions, stream, v.shape[0])
         T = q.shape[0]
         for t, dt in ((q, self.in_dtype), (k, self.in_dtype), (v, self.in_dtype), (g, torch.float32),
                       (beta, torch.float32)):

@@ -166,3 +166,26 @@ def test_structs_match_the_header():
         fields = [f.strip(" *") for line in body.split(";") if line.strip()
                   for f in re.sub(r"^\s*(const )?\w+\s", "", line.strip()).split(",")]
         assert fields == [n for n, _ in struct._fields_], name
+
+
+def state_with_norm(batch=2, heads=4, d=64, **how):
+    """A state's fields without its memory: what its calls check before anything reaches a device."""
+    st = object.__new__(lq.DecodeState)
+    st.__dict__.update(batch=batch, heads=heads, d=d, in_dtype=torch.bfloat16, qk_norm=how, _h=None,
+                       device=torch.device("cpu"))
+    return st
+
+
+@pytest.mark.parametrize("q,k", [((2, 4, 64), (2, 1, 64)), ((2, 4, 64), (2, 4, 32)), ((2, 1, 64), (2, 4, 64)),
+                                 ((1, 4, 64), (1, 4, 64)), ((2, 4, 64), None), ((2, 8, 32), (2, 8, 32))])
+def test_a_state_refuses_queries_and_keys_of_other_heads(q, k):
+    """The norm takes fewer key heads than query heads; the decode kernels read a key a head."""
+    q, k = (None if s is None else torch.zeros(s, dtype=torch.bfloat16) for s in (q, k))
+    v, g = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 4)
+    up = lambda x: None if x is None else torch.stack([x] * 3)  # noqa: E731
+    mask = torch.ones(2, dtype=torch.uint8)
+    st = state_with_norm()
+    for call in (lambda: st.decode_step(q, k, v, g, g), lambda: st.prefill_tokens(up(q), up(k), up(v), up(g), up(g)),
+                 lambda: st.prefill_sequences_tokens(up(q), up(k), up(v), up(g), up(g), mask)):
+        with pytest.raises(AssertionError, match="batch, heads, d"):
+            call()
