@@ -390,10 +390,10 @@ def _qk_inputs(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, 
     pq, tq, hq = _heads_of(q, "q", device, dtype, q.shape)
     pk, tk, hk = _heads_of(k, "k", device, dtype, None if k is None else k.shape)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    assert rot == 0 or positions is not None, "a rotation needs positions"
+    assert (rot == 0) == (positions is None), "a rotation needs positions and inv_freq, both or neither"
     cfg = _pack_qk_config(q.shape[-2], 0 if k is None else k.shape[-2], d, NORM[norm], rot, PAIRS[pairs], DTYPE[dtype],
                           eps, q_scale)
-    args = _pack_qk_args(lead.numel(), pq, pk, _packed(positions, "positions", device, torch.int32, lead) if rot else 0,
+    args = _pack_qk_args(lead.numel(), pq, pk, _packed(positions, "positions", device, torch.int32, lead),
                          _packed(inv_freq, "inv_freq", device, torch.float64, (rot // 2,)),
                          _packed(weight_q, "weight_q", device, torch.float32, (d,)),
                          _packed(weight_k, "weight_k", device, torch.float32, (d,)), tq, hq, tk, hk)
@@ -414,7 +414,7 @@ def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, w
     (BF16 or FP32; views into a fused projection will do), then rotate its
     first 2 * len(inv_freq) channels by positions * inv_freq and multiply q by
     q_scale (lq_qk_norm_rotate).  norm: "l2" or "rms"; weights FP32 [d] (None:
-    1); positions int32 [...]; inv_freq FP64 [rot_dim / 2] (None: no
+    1); positions int32 [...] and inv_freq FP64 [rot_dim / 2] (both None: no
     rotation); pairs: "half" (i with i + rot_dim / 2) or "neighbours" (2 i
     with 2 i + 1).  Returns (q_out, k_out), new tensors unless given; they may
     be q and k themselves."""

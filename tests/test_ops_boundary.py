@@ -189,3 +189,39 @@ def test_a_state_refuses_queries_and_keys_of_other_heads(q, k):
                  lambda: st.prefill_sequences_tokens(up(q), up(k), up(v), up(g), up(g), mask)):
         with pytest.raises(AssertionError, match="batch, heads, d"):
             call()
+
+
+@pytest.fixture
+def host_tensors_pass(monkeypatch):
+    """The binding's checks on host tensors, up to the library call (which the test sees refused or made)."""
+    monkeypatch.setattr(lq, "_on", lambda x, stream: None)
+    monkeypatch.setattr(lq, "_raw_stream", lambda device: 0)
+
+    class Library:
+        calls = []
+
+        def __getattr__(self, name):
+            if name.endswith("_bytes"):
+                return lambda *a: 64
+            return lambda *a: self.calls.append(name) or lq.LQ_OK
+
+    fake = Library()
+    fake.calls.clear()
+    monkeypatch.setattr(lq, "lib", lambda: fake)
+    return fake.calls
+
+
+def test_positions_and_frequencies_go_together(host_tensors_pass):
+    q, pos = torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int32)
+    freq = torch.ones(16, dtype=torch.float64)
+    for how in ({"positions": pos}, {"inv_freq": freq}, {"positions": pos, "inv_freq": freq[:0]}):
+        for call in (lambda: lq.qk_norm_rotate(q, q, **how), lambda: lq.qk_norm_rotate_backward(q, q, q, q, **how)):
+            with pytest.raises(AssertionError, match="positions and inv_freq"):
+                call()
+    st = state_with_norm(batch=3, heads=2)
+    with pytest.raises(AssertionError, match="positions and inv_freq"):
+        st.decode_step(q, q, q, q[..., 0], q[..., 0], positions=pos)
+    assert host_tensors_pass == []
+    lq.qk_norm_rotate(q, q, positions=pos, inv_freq=freq)
+    lq.qk_norm_rotate(q, q)
+    assert host_tensors_pass == ["lq_qk_norm_rotate"] * 2
