@@ -225,6 +225,16 @@ def _on(x: torch.Tensor, stream):
     return torch.cuda.stream(stream)
 
 
+def _outside_autograd(*tensors):
+    """Refuse tensors that autograd would follow: the results have no graph,
+    and the gradients are calls of their own."""
+    if torch.is_grad_enabled():
+        for x in tensors:
+            assert x is None or not x.requires_grad, \
+                "a tensor requires a gradient, which autograd would not get through this call: call it under " \
+                "torch.no_grad() or in an autograd.Function, with the operator's backward call for the gradients"
+
+
 # the current stream's handle without a Stream object where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -299,6 +309,7 @@ def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None,
     last token.  `out` and `h_last` may be given (rows of `out` past a length
     then stay as they are; h_last may be h0); want_out=False skips `out`.
     `checkpoints` (gated_scan_checkpoints()) is filled for the backward pass."""
+    _outside_autograd(v, g, beta, h0)
     on = _on(v, stream)
     if on is not None:
         with on:
@@ -330,6 +341,7 @@ def gated_scan_backward(grad_out, v, g, beta=None, *, checkpoints, grad_last=Non
     (grad_v, grad_g, grad_beta, grad_h0); grad_beta is None without beta.
     Tokens past a length get zero, or stay as they are in a tensor given for
     the result."""
+    _outside_autograd(grad_out, grad_last, v, g, beta)
     on = _on(v, stream)
     if on is not None:
         with on:
@@ -418,6 +430,7 @@ def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, w
     rotation); pairs: "half" (i with i + rot_dim / 2) or "neighbours" (2 i
     with 2 i + 1).  Returns (q_out, k_out), new tensors unless given; they may
     be q and k themselves."""
+    _outside_autograd(q, k, weight_q, weight_k)
     on = _on(q, stream)
     if on is not None:
         with on:
@@ -441,6 +454,7 @@ def qk_norm_rotate_backward(grad_q_out, grad_k_out, q, k=None, *, positions=None
     the keywords as in the forward call, grad_q_out and grad_k_out those of
     its results.  Returns (grad_q, grad_k, grad_weight_q, grad_weight_k), the
     last two FP32 [d], None where there is no weight (or are no keys)."""
+    _outside_autograd(grad_q_out, grad_k_out, q, k, weight_q, weight_k)
     on = _on(q, stream)
     if on is not None:
         with on:
@@ -530,7 +544,8 @@ class DecodeState:
             assert x is not None and x.shape[-2:] == (self.heads, self.d) and \
                 x.numel() == n_tokens * self.batch * self.heads * self.d, \
                 f"q and k are [batch, heads, d], for a prompt [T, batch, heads, d]: {None if x is None else tuple(x.shape)}"
-        return qk_norm_rotate(q, k, positions=positions, stream=stream, **self.qk_norm)
+        with torch.no_grad():       # a state's results have no gradients
+            return qk_norm_rotate(q, k, positions=positions, stream=stream, **self.qk_norm)
 
     def decode_step(self, q, k, v, g, beta, out: torch.Tensor | None = None, stream=None,
                     active: torch.Tensor | None = None, positions: torch.Tensor | None = None) -> torch.Tensor:

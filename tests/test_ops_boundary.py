@@ -225,3 +225,25 @@ def test_positions_and_frequencies_go_together(host_tensors_pass):
     lq.qk_norm_rotate(q, q, positions=pos, inv_freq=freq)
     lq.qk_norm_rotate(q, q)
     assert host_tensors_pass == ["lq_qk_norm_rotate"] * 2
+
+
+def test_tensors_that_autograd_follows_are_refused(host_tensors_pass):
+    """The results have no graph, so a loss on them would leave the leaves without a gradient."""
+    leaf = lambda *s: torch.zeros(*s, requires_grad=True)  # noqa: E731
+    q, w, g, h, m = torch.zeros(3, 2, 4, 64), torch.zeros(64), torch.zeros(3, 2, 4), torch.zeros(2, 4, 64), torch.zeros(99)
+    ql, wl, gl, hl = leaf(3, 2, 4, 64), leaf(64), leaf(3, 2, 4), leaf(2, 4, 64)
+    calls = [lambda: lq.gated_scan(ql, g), lambda: lq.gated_scan(q, gl), lambda: lq.gated_scan(q, g, gl),
+             lambda: lq.gated_scan(q, g, g, hl), lambda: lq.gated_scan_backward(ql, q, g, checkpoints=m),
+             lambda: lq.gated_scan_backward(q, ql, g, checkpoints=m), lambda: lq.qk_norm_rotate(ql, q),
+             lambda: lq.qk_norm_rotate(q, ql), lambda: lq.qk_norm_rotate(q, q, weight_q=w, weight_k=wl),
+             lambda: lq.qk_norm_rotate_backward(q, q, q, ql), lambda: lq.qk_norm_rotate_backward(q, ql, q, q)]
+    for call in calls:
+        with pytest.raises(AssertionError, match="requires a gradient"):
+            call()
+    assert host_tensors_pass == []
+    with torch.no_grad():
+        for call in calls:
+            call()
+    assert len(host_tensors_pass) == len(calls)
+    st = state_with_norm(batch=2, heads=4, weight_q=wl)       # a state's calls have no gradients either way
+    assert all(not x.requires_grad for x in st._normed(ql[0], q[0], None, None))
