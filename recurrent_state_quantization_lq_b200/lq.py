@@ -265,6 +265,13 @@ def _rows(x: torch.Tensor | None, what: str, device: int, dtype, shape):
     return x.data_ptr(), s[:3]
 
 
+def _result_like(x: torch.Tensor, dtype=None, make=torch.empty_like) -> torch.Tensor:
+    """A tensor for results like x, in x's order where that leaves the channels
+    contiguous (views whose tokens overlap may have none)."""
+    y = make(x, dtype=dtype)
+    return y if x.dim() < 4 or y.stride(3) == 1 else make(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _scan_config(v: torch.Tensor, g: torch.Tensor, out_dtype) -> bytes:
     assert v.dim() == 4, "v is [T, batch, heads, d]"
     T, B, H, d = v.shape
@@ -321,7 +328,7 @@ def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None,
     pv, pg, pb, pl, pc, sv, sg, sb = _scan_inputs(v, g, beta, lengths, checkpoints, cfg, device)
     zero_past = out is None
     if zero_past and want_out:
-        out = torch.empty_like(v, dtype=out_dtype)
+        out = _result_like(v, out_dtype)
     if h_last is None:
         h_last = v.new_empty(states, dtype=torch.float32)
     po, so = _rows(out, "out", device, out_dtype, v.shape)
@@ -354,11 +361,11 @@ def gated_scan_backward(grad_out, v, g, beta=None, *, checkpoints, grad_last=Non
     pv, pg, pb, pl, pc, sv, sg, sb = _scan_inputs(v, g, beta, lengths, checkpoints, cfg, device)
     # rows past a length: zeroed by the kernel, unless a given tensor is to keep its own
     zero_past = grad_v is None and grad_g is None and grad_beta is None
-    new = torch.empty_like if zero_past or lengths is None else torch.zeros_like
-    grad_v = new(v) if grad_v is None else grad_v
-    grad_g = new(g) if grad_g is None else grad_g
+    make = torch.empty_like if zero_past or lengths is None else torch.zeros_like
+    grad_v = _result_like(v, None, make) if grad_v is None else grad_v
+    grad_g = _result_like(g, None, make) if grad_g is None else grad_g
     if beta is not None and grad_beta is None:
-        grad_beta = new(beta)
+        grad_beta = _result_like(beta, None, make)
     if grad_h0 is None:
         grad_h0 = v.new_empty(states, dtype=torch.float32)
     py, sy = _rows(grad_out, "grad_out", device, out_dtype, v.shape)

@@ -247,3 +247,15 @@ def test_tensors_that_autograd_follows_are_refused(host_tensors_pass):
     assert len(host_tensors_pass) == len(calls)
     st = state_with_norm(batch=2, heads=4, weight_q=wl)       # a state's calls have no gradients either way
     assert all(not x.requires_grad for x in st._normed(ql[0], q[0], None, None))
+
+
+@pytest.mark.parametrize("strides", [(2, 0, 0, 1), (1, 0, 0, 1), (8, 16, 4, 1), (24, 120, 8, 1)])
+def test_inputs_whose_tokens_overlap_are_taken(host_tensors_pass, strides):
+    """Sliding windows over a sequence are views with contiguous channels like any other."""
+    v = torch.zeros(1000).as_strided((5, 2, 3, 8), strides)
+    out, _ = lq.gated_scan(v, v)
+    gv, gg, _, _ = lq.gated_scan_backward(v, v, v, checkpoints=v.new_empty(64))
+    for x in (out, gv, gg):
+        assert x.shape == v.shape and x.stride(3) == 1 and len({x[i].data_ptr() for i in range(5)}) == 5
+    if strides == (24, 120, 8, 1):                       # what is dense keeps its order
+        assert out.stride() == gv.stride() == v.stride()
