@@ -161,7 +161,9 @@ lq_status lq_gated_scan_backward(const lq_scan_config *cfg, const lq_scan_args *
         !strides_cover(grads->grad_beta, grads->grad_beta_stride, T, B, H))
         return fail(LQ_ERR_INVALID_ARG, "an output dimension has stride 0");
     const Extent x{T, B, H, cfg->d};
-    vec = vec && rows_of_16_bytes(grads->grad_out, grads->grad_out_stride, x, element(cfg->out_dtype)) &&
+    // (a grad_out that is not there has rows in shared memory all the same, which the kernel clears)
+    vec = vec && cfg->d * element(cfg->out_dtype) % 16 == 0 &&
+          rows_of_16_bytes(grads->grad_out, grads->grad_out_stride, x, element(cfg->out_dtype)) &&
           rows_of_16_bytes(grads->grad_v, grads->grad_v_stride, x, element(cfg->in_dtype)) &&
           (cfg->gate != LQ_GATE_CHANNEL || rows_of_16_bytes(grads->grad_g, grads->grad_g_stride, x, 4));
     const cudaError_t e = lq::launch_scan_backward(*cfg, *args, *grads, vec, static_cast<cudaStream_t>(stream));

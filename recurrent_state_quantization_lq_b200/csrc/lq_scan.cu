@@ -915,8 +915,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
 #pragma unroll 1
                 for (int i = live; i < R; ++i) {
                     clear_shared<InT>(base, pitch, row * R + i, c0, n);
-                    // (without grad_out its area is not read, and its rows may be half pieces of 16 bytes)
-                    if (py != nullptr) clear_shared<OutT>(base + y_at, pitch, row * R + i, c0, n);
+                    clear_shared<OutT>(base + y_at, pitch, row * R + i, c0, n);     // (without grad_out too: whole pieces)
                     if (CHAN) clear_shared<float>(base + gates_at, pitch, row * R + i, c0, n);
                 }
                 fence_proxy_async_smem();
