@@ -306,10 +306,22 @@ __device__ __forceinline__ void init_bars(Bars &b, int workers) {
     fence_mbar_init();
 }
 
-// Every wait is bounded.  After one that ran out, what follows is NaN (tokens or
-// a peer's map never came) and the later waits, for the copies still on their
-// way, are short.
-__device__ __forceinline__ long long budget_of(bool alive) { return alive ? kWaitBudgetCycles : 200000LL; }
+// Every wait is bounded.  After one that ran out (tokens or a peer's map never
+// came) the later ones are short, and what came too late or depends on it is
+// NaN: forward the tokens from the late ones on, backward the late tokens, what
+// their gradient reaches before them and grad_g behind them in the same step.
+constexpr long long kLateCycles = 200000;
+__device__ __forceinline__ long long budget_of(bool alive) { return alive ? kWaitBudgetCycles : kLateCycles; }
+// Before the CTA's end: late copies, which still write to its stages, get time to land.
+__device__ __forceinline__ void linger() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kLateCycles) {}
+}
+
+__device__ __forceinline__ void fill_nan(float2 (&x)[4], float2 (&y)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = y[c] = make_float2(nanf(""), nanf(""));
+}
 
 // The stage of a step and the parity of its use, counted without divisions.
 struct Turn {
@@ -603,6 +615,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
         int mark = (rank * chunk + row * R) / every, past_mark = rank * chunk + row * R - mark * every;
         Gates<CHAN> A_before;        // of the step whose pass two is due: the map of its warp's rows before this one
         float2 H_before[4];
+        bool alive_before = true;    // (as the maps: of that step)
         for (int s = 0; s <= steps; ++s) {
             Gates<CHAN> A;
             float2 H[4] = {};
@@ -613,7 +626,6 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
                 float2 *sc = reinterpret_cast<float2 *>(base + space.scalars()) + row * R;
                 float *sH = maps + (s & 1) * space.map(), *sA = sH + NW * dp;
                 alive = mbar_wait(&bars.full[one.stage], one.parity, budget_of(alive)) && alive;
-                if (!alive) A.fill(nanf(""));
                 // each gate is raised once, by one lane of its row; past the end it is 1, and beta 0
                 for (int i = in_row; i < R; i += lanes) {
                     if (!CHAN) sc[i].x = i < live ? gate_of(sc[i].x) : 1.0f;
@@ -647,6 +659,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
                     for (int c = 0; c < 4; ++c) H[c] = fma2(gate[c], H[c], mul2(make_float2(gb.y, gb.y), v[c]));
                     A.times(gate);
                 }
+                if (!alive) fill_nan(H, H);          // the row's map, and with it every later state
                 for (int o = lanes; o < 32; o *= 2) {
                     const Gates<CHAN> before = A.before(o);
 #pragma unroll
@@ -676,6 +689,7 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (lane >= lanes) h[c] = fma2(A_before[c], h[c], H_before[c]);
+                if (!alive_before) fill_nan(h, h);
                 if (a.checkpoints != nullptr) {
                     if (on && live > 0 && past_mark == 0)
                         store8<VEC>(a.checkpoints + ((int64_t)mark * units + w.u) * d + c0, n, h);
@@ -708,9 +722,11 @@ __global__ void __launch_bounds__(32 * forward_warps(CHAN) + 64, 2)
                 two.next();
             }
             A_before = A;
+            alive_before = alive;
 #pragma unroll
             for (int c = 0; c < 4; ++c) H_before[c] = H[c];
         }
+        if (!alive) linger();
         if (a.zero_past && a.out != nullptr && on) {
             const float2 zero[4] = {};
 #pragma unroll 1
@@ -910,7 +926,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
             A.fill(1.0f);
             B.fill(1.0f);
             alive = mbar_wait(&bars.full[turn.stage], turn.parity, budget_of(alive)) && alive;
-            if (!alive) A.fill(nanf(""));
+            if (!alive) fill_nan(H, E);              // the row's results and its maps
             if (live < R && on) {                    // what lies past the sequence's end is nothing
 #pragma unroll 1
                 for (int i = live; i < R; ++i) {
@@ -1129,6 +1145,7 @@ __global__ void __launch_bounds__(32 * kBackwardWarps + 32, D_ > 0 ? 2 : 1)
             if (!VEC) bring(s + kStages, turn.stage);
             turn.next();
         }
+        if (!alive) linger();
         if (a.zero_past && on) {
             const float2 zero[4] = {};
 #pragma unroll 1
