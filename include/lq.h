@@ -443,7 +443,8 @@ typedef struct lq_scan_args {
                                   1 set to zero                                   */
     const void *v;             /* in_dtype [T][batch][heads][d], any strides      */
     const float *g;            /* f32 [T][batch][heads] or [..][d]: log alpha,
-                                  <= 0 in ordinary use (-inf empties the state)   */
+                                  <= 0 in ordinary use (-inf empties the state);
+                                  see below for growing states                    */
     const float *beta;         /* f32 [T][batch][heads]; NULL: 1                  */
     const float *h0;           /* f32 [batch][heads][d]: start; NULL: zero        */
     const int32_t *lengths;    /* int32 [batch]: tokens of each sequence, clamped
@@ -479,6 +480,13 @@ LQ_API size_t lq_gated_scan_checkpoint_bytes(const lq_scan_config *cfg, int32_t 
  * sequence, or (n_tokens = 1) one decode token.  Long sequences are split over
  * the device.  With `checkpoints` it leaves there what the backward pass needs
  * besides the inputs.
+ * Range: the gates of a run of tokens are multiplied before they meet a state,
+ * so g may sum to 80 at most over any consecutive tokens of a sequence (as
+ * g <= 0 always does; there is no lower limit).  Beyond, that head's (channel's)
+ * results after the run, and its gradients before and after it, are undefined
+ * and may be infinite or NaN where the recurrence itself stays finite, for
+ * example over a state of zeros.  An infinity or NaN in v or h0 leaves its
+ * channel infinite or NaN from there to the sequence's end, and no other.
  * Errors: LQ_ERR_INVALID_ARG for a bad config field, a NULL v or g with
  * n_tokens > 0, an n_tokens out of range, a pointer not aligned to its element or
  * an output dimension of stride 0.
@@ -518,8 +526,10 @@ enum {
  * then the first rot_dim channels turn in pairs by the angles
  * theta_i = position * inv_freq[i],
  *     (u_a, u_b) -> (u_a cos theta_i - u_b sin theta_i, u_b cos theta_i + u_a sin theta_i),
- * and q is multiplied by q_scale.  FP32 inside, rounded once; the angles are
- * formed in FP64, so positions up to 2^31 - 1 keep FP32 accuracy.
+ * and q is multiplied by q_scale.  FP32 inside, rounded once.  x may reach 1e18
+ * in size; a row whose sum of squares passes FP32's range is not normalised (its
+ * results and gradients are zero or NaN).  The angles are formed in FP64, so
+ * positions up to 2^31 - 1 keep FP32 accuracy.
  */
 typedef struct lq_qk_norm_config {
     int32_t heads_q;      /* query heads, >= 1                                   */

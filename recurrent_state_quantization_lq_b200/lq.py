@@ -309,7 +309,8 @@ def gated_scan(v, g, beta=None, h0=None, *, lengths=None, out=None, h_last=None,
     """The gated linear recurrence h_t = exp(g_t) h_{t-1} + beta_t v_t over
     vector states (lq_gated_scan): v [T, batch, heads, d] (BF16 or FP32, any
     strides with contiguous channels; transpose a [batch, T, ...] tensor), g
-    FP32 [T, batch, heads] or [T, batch, heads, d], beta FP32 [T, batch, heads]
+    FP32 [T, batch, heads] or [T, batch, heads, d] (its sum over consecutive
+    tokens at most 80, as g <= 0 always has it), beta FP32 [T, batch, heads]
     (None: 1), h0 FP32 [batch, heads, d] (None: zero), lengths int32 [batch]
     on the device (None: T).  Returns (out, h_last): every h_t in out_dtype
     (default v's), zero past a sequence's length, and the FP32 state after its
