@@ -1,4 +1,5 @@
-"""Accuracy of the q/k norm where many bits count: far positions."""
+"""Accuracy of the q/k norm where many bits count: far positions, and weight
+gradients over more tokens than the backward kernel takes in one round."""
 from fractions import Fraction
 
 import pytest
@@ -9,6 +10,7 @@ from recurrent_state_quantization_lq_b200 import lq
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
 TWO_PI = 2 * Fraction(31415926535897932384626433832795028841971693993751058209749445923, 10 ** 64)
 
 
@@ -41,3 +43,55 @@ def test_angles_keep_fp32_accuracy_at_any_position(pairs, rot, near):
     off = torch.atan2(y[:, second], y[:, first]) - want
     off = (off - 2 * torch.pi * torch.round(off / (2 * torch.pi))).abs()
     assert off.max() <= 3 * 2 ** 0.5 * plain_ops.U, float(off.max()) / plain_ops.U
+
+
+def test_weight_gradients_round_once_over_the_tokens():
+    """Rows of ones are their own norm, so dw = sum over the rows of dy.  With gradients of 18 bits a CTA's part (8 row
+    groups of one or two rows) is exact in FP32; the sum over the CTAs is not, and must be rounded once."""
+    M, d = 9000, 256
+    gen = torch.Generator().manual_seed(1)
+    x = torch.ones(M, 1, d, device=DEV)
+    dy = ((2 ** 17 + torch.randint(0, 2 ** 17, (M, 1, d), generator=gen)).double() / 2 ** 17).to(F32).to(DEV)
+    w = torch.ones(d, device=DEV)
+    how = {"norm": "rms", "eps": 1e-30, "weight_q": w, "weight_k": w}
+    for y in lq.qk_norm_rotate(x, x, **how):
+        assert (y == 1).all()
+    _, _, gwq, gwk = lq.qk_norm_rotate_backward(dy, dy, x, x, **how)
+    want = dy.double().sum((0, 1)).to(F32)
+    assert torch.equal(gwq, want) and torch.equal(gwk, want)
+
+
+@pytest.mark.parametrize("M,hq,hk,d,rot,pairs", [(8192 + 5, 1, 1, 256, 256, "half"), (16384 + 3, 1, 2, 128, 128, "half"),
+                                                 (16384 + 3, 2, 1, 128, 64, "neighbours"), (32768 + 9, 1, 1, 64, 36, "half"),
+                                                 (2 * 16384 + 1, 1, 0, 100, 24, "half"), (2 * 32768 + 77, 2, 1, 50, 0, "half")])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_tokens_than_one_round_of_the_backward_kernel(M, hq, hk, d, rot, pairs, dtype):
+    """The grid is capped at 1024 CTAs (1024 x 8, 16 or 32 rows): threads carry their weight gradients over rounds,
+    the last of which is partly dead.  dw is held to the additions that are made: a thread's rows, one by one, and
+    three roundings of larger sums.  One row's part is 1 / (M heads) of the sum, 15 times the bound and more."""
+    gen = torch.Generator().manual_seed(M)
+    on = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(DEV)  # noqa: E731
+    q, gq = on(M, hq, d), on(M, hq, d)
+    k, gk = (on(M, hk, d), on(M, hk, d)) if hk else (None, None)
+    how = {"norm": "rms", "pairs": pairs, "q_scale": 0.5, "weight_q": torch.randn(d, generator=gen).to(DEV)}
+    if hk:
+        how["weight_k"] = torch.randn(d, generator=gen).to(DEV)
+    if rot:
+        how["positions"] = torch.randint(0, 5000, (M,), generator=gen, dtype=torch.int32).to(DEV)
+        how["inv_freq"] = (10000.0 ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / rot)).to(DEV)
+    got = lq.qk_norm_rotate_backward(gq, gk, q, k, **how)
+    lanes = 1
+    while 8 * lanes < d:
+        lanes *= 2
+    rounds = -(-M // (1024 * (256 // lanes)))
+    assert rounds > 1
+    for i, (x, dy, heads, scale) in enumerate(((q, gq, hq, 0.5), (k, gk, hk, 1.0))):
+        if x is None:
+            continue
+        want = plain_ops.qk(x, how.get("positions"), how.get("inv_freq"), how["weight_" + "qk"[i]], "rms", 1e-6, pairs,
+                            scale, dy)
+        assert torch.isfinite(got[i]).all() and torch.isfinite(got[2 + i]).all()
+        plain_ops.check(got[i], want["dx"], dtype, "dx")
+        value, loose = want["dw"]
+        C = 2 * plain_ops.C_QK
+        plain_ops.check(got[2 + i], (value, loose * (C + rounds * heads + 3) / (C + M * heads)), F32, "dw")
