@@ -68,7 +68,8 @@ def test_weight_gradients_round_once_over_the_tokens():
 def test_more_tokens_than_one_round_of_the_backward_kernel(M, hq, hk, d, rot, pairs, dtype):
     """The grid is capped at 1024 CTAs (1024 x 8, 16 or 32 rows): threads carry their weight gradients over rounds,
     the last of which is partly dead.  dw is held to the additions that are made: a thread's rows, one by one, and
-    three roundings of larger sums.  One row's part is 1 / (M heads) of the sum, 15 times the bound and more."""
+    three roundings of larger sums: (48 + at most 9) u of the sum of absolute values, 3.4e-6.  One row's part is
+    1 / (M heads) of that sum, 7.6e-6 and more."""
     gen = torch.Generator().manual_seed(M)
     on = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(DEV)  # noqa: E731
     q, gq = on(M, hq, d), on(M, hq, d)
