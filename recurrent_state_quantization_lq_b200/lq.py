@@ -439,11 +439,15 @@ def qk_norm_rotate(q, k=None, *, positions=None, inv_freq=None, weight_q=None, w
     with 2 i + 1).  Returns (q_out, k_out), new tensors unless given; they may
     be q and k themselves."""
     _outside_autograd(q, k, weight_q, weight_k)
+    return _qk_norm_rotate(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale, q_out, k_out, stream)
+
+
+def _qk_norm_rotate(q, k, positions=None, inv_freq=None, weight_q=None, weight_k=None, norm="l2", eps=1e-6, pairs="half",
+                    q_scale=1.0, q_out=None, k_out=None, stream=None):
     on = _on(q, stream)
     if on is not None:
         with on:
-            return qk_norm_rotate(q, k, positions=positions, inv_freq=inv_freq, weight_q=weight_q, weight_k=weight_k,
-                                  norm=norm, eps=eps, pairs=pairs, q_scale=q_scale, q_out=q_out, k_out=k_out)
+            return _qk_norm_rotate(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale, q_out, k_out)
     cfg, args = _qk_inputs(q, k, positions, inv_freq, weight_q, weight_k, norm, eps, pairs, q_scale)
     if q_out is None:
         q_out = q.new_empty(q.shape)
@@ -552,8 +556,7 @@ class DecodeState:
             assert x is not None and x.shape[-2:] == (self.heads, self.d) and \
                 x.numel() == n_tokens * self.batch * self.heads * self.d, \
                 f"q and k are [batch, heads, d], for a prompt [T, batch, heads, d]: {None if x is None else tuple(x.shape)}"
-        with torch.no_grad():       # a state's results have no gradients
-            return qk_norm_rotate(q, k, positions=positions, stream=stream, **self.qk_norm)
+        return _qk_norm_rotate(q, k, positions, stream=stream, **self.qk_norm)     # (no state's call has gradients)
 
     def decode_step(self, q, k, v, g, beta, out: torch.Tensor | None = None, stream=None,
                     active: torch.Tensor | None = None, positions: torch.Tensor | None = None) -> torch.Tensor:
