@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(kQkThreads, 4)
 }
 
 // A sum in two FP32 parts: the second has what the additions to the first round
-// off (Knuth's two-sum).  The weight gradients' sums of many parts, over a CTA's
-// rows and over the CTAs, are taken so, and their error does not grow with the
-// tokens.  A thread's own sum, one head or more of each of its tokens, is plain
-// FP32: its registers are full.  (16384 tokens of 40 heads, forward and backward:
-// 191 us, with plain sums 189, in FP64 192.)
+// off (Knuth's two-sum).  The weight gradients' sums of many parts, over a
+// thread's rounds, a CTA's rows and the CTAs, are taken so, and their error does
+// not grow with the tokens.  A thread's sum over up to kPlainRows rows (or the
+// heads of one token) is plain FP32: its registers are full, and what it carries
+// over rounds lies in shared memory.
 struct TwoSum {
     float s = 0.0f, e = 0.0f;
     __device__ __forceinline__ void add(float x, float rest = 0.0f) {
@@ -280,6 +280,12 @@ struct TwoSum {
     }
     __device__ __forceinline__ float value() const { return isfinite(s) ? s + e : s; }
 };
+constexpr int kPlainRows = 32;
+// The rounds of the backward kernel whose rows a thread adds up plainly.
+__host__ __device__ inline int rounds_of_plain_sums(int heads, int split) {
+    const int per_round = (heads + split - 1) / split;
+    return per_round < kPlainRows ? kPlainRows / per_round : 1;
+}
 
 template <typename T, bool VEC, int ROT, int LANES>
 __global__ void __launch_bounds__(kQkThreads, 3)
@@ -287,6 +293,7 @@ __global__ void __launch_bounds__(kQkThreads, 3)
                             int any_lanes, int split, int64_t groups) {
     const int lanes = LANES > 0 ? LANES : any_lanes;
     __shared__ __align__(16) float rows[kQkThreads * 8];
+    extern __shared__ float2 sums[];             // the threads' parts over the rounds (a TwoSum each), where carried
     float *row = rows + (threadIdx.x / lanes) * lanes * 8;
     const int64_t first = ((int64_t)blockIdx.x * kQkThreads + threadIdx.x) / lanes;
     const int64_t all = (int64_t)gridDim.x * (kQkThreads / lanes);
@@ -299,7 +306,11 @@ __global__ void __launch_bounds__(kQkThreads, 3)
     const float scale = is_q ? c.q_scale : 1.0f;          // of the results: they are linear in dy
     const int64_t x_head = is_q ? a.q_head : a.k_head, y_head = is_q ? gy.q_head : gy.k_head,
                   z_head = is_q ? gx.q_head : gx.k_head;
-    float2 dw[4] = {};                    // this thread's part of the weight gradient
+    float2 dw[4] = {};                    // this thread's part of the weight gradient: of `every` rounds
+    const int every = rounds_of_plain_sums(heads, split);
+    const bool carried = partials != nullptr && rounds > every;
+    if (carried)
+        for (int i = 0; i < 8; ++i) sums[i * kQkThreads + threadIdx.x] = make_float2(0.0f, 0.0f);
     for (int64_t round = 0; round < rounds; ++round) {
         Share s = share_of(c.d, lanes, split, first + round * all);
         const bool live = s.m < a.n_tokens;
@@ -346,6 +357,17 @@ __global__ void __launch_bounds__(kQkThreads, 3)
             for (int i = 0; i < 4; ++i) du[i] = mul2(make_float2(rs, rs), fma2(make_float2(dot, dot), xh[i], du[i]));
             if (mine && s.on) store8<VEC>(z, s.n, du);
             z += split * z_head;
+        }
+        if (carried && ((round + 1) % every == 0 || round + 1 == rounds)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 so_far = sums[i * kQkThreads + threadIdx.x];
+                TwoSum t{so_far.x, so_far.y};
+                float &x = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+                t.add(x);
+                sums[i * kQkThreads + threadIdx.x] = make_float2(t.s, t.e);
+                x = round + 1 < rounds ? 0.0f : t.value();
+            }
         }
     }
     if (partials == nullptr) return;
@@ -452,11 +474,15 @@ cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm
     const bool sums = gwq != nullptr || gwk != nullptr;
     const unsigned grid = (unsigned)(want < kQkPartials ? want : kQkPartials);
     if (grid > 0) {
+        const int64_t rounds = (want + grid - 1) / grid;
+        const bool carried = sums && (rounds > rounds_of_plain_sums(c.heads_q, split) ||
+                                      (c.heads_k > 0 && rounds > rounds_of_plain_sums(c.heads_k, split)));
+        const int smem = carried ? 8 * kQkThreads * (int)sizeof(float2) : 0;
         const cudaError_t e = by_kind(c, vec, [&](auto k) {
             using K = decltype(k);
             qk_norm_backward_kernel<typename K::Type, K::V, K::R, K::LANES>
-                <<<dim3(grid, c.heads_k > 0 ? 2 : 1), kQkThreads, 0, s>>>(c, a, gy, gx, sums ? partials : nullptr, lanes, split,
-                                                                         groups);
+                <<<dim3(grid, c.heads_k > 0 ? 2 : 1), kQkThreads, smem, s>>>(c, a, gy, gx, sums ? partials : nullptr, lanes,
+                                                                            split, groups);
             return cudaGetLastError();
         });
         if (e != cudaSuccess) return e;

@@ -61,6 +61,19 @@ def test_weight_gradients_round_once_over_the_tokens():
     assert torch.equal(gwq, want) and torch.equal(gwk, want)
 
 
+@pytest.mark.parametrize("heads,rounds", [(1, 64), (4, 16), (48, 2)])
+def test_weight_gradients_do_not_lose_more_with_the_rounds(heads, rounds):
+    """Rows of ones and one gradient everywhere: dw = M heads g.  A thread takes heads x rounds rows, and for this g
+    plain FP32 additions round with one sign, up to 0.5 u of each partial sum: n of them leave up to
+    sum_i 0.5 u i / n = 0.25 (n + 1) u, the same in every thread.  Allowed: that of 32 rows, or of one token's heads,
+    and the roundings of the thread's sum, of the CTA's and of the result, 1.5 u."""
+    M, d, g = rounds * 8192, 256, float.fromhex("0x1.f08ccp+0")
+    x, dy, w = torch.ones(M, heads, d, device=DEV), torch.full((M, heads, d), g, device=DEV), torch.ones(d, device=DEV)
+    gw = lq.qk_norm_rotate_backward(dy, None, x, norm="rms", eps=1e-30, weight_q=w)[2]
+    off = (gw.double().cpu() / (M * heads * g) - 1).abs().max()
+    assert off <= (0.25 * (max(32, heads) + 1) + 1.5) * plain_ops.U, float(off) / plain_ops.U
+
+
 @pytest.mark.parametrize("M,hq,hk,d,rot,pairs", [(8192 + 5, 1, 1, 256, 256, "half"), (16384 + 3, 1, 2, 128, 128, "half"),
                                                  (16384 + 3, 2, 1, 128, 64, "neighbours"), (32768 + 9, 1, 1, 64, 36, "half"),
                                                  (2 * 16384 + 1, 1, 0, 100, 24, "half"), (2 * 32768 + 77, 2, 1, 50, 0, "half")])
