@@ -408,7 +408,9 @@ LQ_API lq_status lq_state_destroy(lq_handle h);
  * as neither writes what the other reads or writes (workspaces and
  * checkpoints included).  Outputs must not overlap inputs or other outputs
  * except where a field says so.  They report no device errors: masks,
- * lengths and values outside the stated ranges are handled as stated here.
+ * lengths and values outside the stated ranges are handled as stated here, and
+ * a bounded wait that expires (after about a second) leaves NaN in the results
+ * that it was for.
  * Each is the same from run to run on the same inputs (no atomics).
  * ---------------------------------------------------------------------- */
 
