@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(kQkThreads, 4)
 // A sum in two FP32 parts: the second has what the additions to the first round
 // off (Knuth's two-sum).  The weight gradients' sums of many parts, over a
 // thread's rounds, a CTA's rows and the CTAs, are taken so, and their error does
-// not grow with the tokens.  A thread's sum over up to kPlainRows rows (or the
-// heads of one token) is plain FP32: its registers are full, and what it carries
-// over rounds lies in shared memory.
+// not grow with the tokens.  Up to kPlainRows rows of a thread (or the heads of
+// one token), and as many threads' parts, are added up in plain FP32: a thread's
+// registers are full, and what it carries over rounds lies in shared memory.
 struct TwoSum {
     float s = 0.0f, e = 0.0f;
     __device__ __forceinline__ void add(float x, float rest = 0.0f) {
@@ -379,18 +379,25 @@ __global__ void __launch_bounds__(kQkThreads, 3)
     __syncthreads();
     for (int e = threadIdx.x; e < c.d; e += kQkThreads) {
         TwoSum t;
-        for (int i = 0; i < n_rows; ++i) t.add(rows[i * dp + e]);
+        for (int i0 = 0; i0 < n_rows; i0 += kPlainRows) {
+            float x = 0.0f;
+            for (int i = i0; i < min(i0 + kPlainRows, n_rows); ++i) x += rows[i * dp + e];
+            t.add(x);
+        }
         partials[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * c.d + e] = scale * t.value();
     }
 }
 
-// grad_weight[e] = the sum of the CTAs' parts; one CTA for 32 channels of each
-// of q and k, 32 threads a channel.
-__global__ void __launch_bounds__(1024) qk_weight_sum_kernel(const float *partials, int n, int d, float *gwq, float *gwk) {
-    __shared__ float part[32][33], rest[32][33];
+// grad_weight[e] = the sum of the CTAs' parts; one CTA for eight channels of each
+// of q and k, 32 threads a channel.  (With 32 channels a CTA the two-part sums of
+// its 1024 threads took 1 us more than plain ones; so they take none.)
+constexpr int kSumChannels = 8;
+__global__ void __launch_bounds__(32 * kSumChannels)
+    qk_weight_sum_kernel(const float *partials, int n, int d, float *gwq, float *gwk) {
+    __shared__ float part[kSumChannels][33], rest[kSumChannels][33];
     float *dst = blockIdx.y == 0 ? gwq : gwk;
     if (dst == nullptr) return;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + x;
+    const int x = threadIdx.x % kSumChannels, y = threadIdx.x / kSumChannels, e = blockIdx.x * kSumChannels + x;
     TwoSum s;
     constexpr int AHEAD = 8;         // parts in flight; one at a time took 10 us more
     const float *from = partials + (int64_t)blockIdx.y * n * d + min(e, d - 1);
@@ -404,9 +411,10 @@ __global__ void __launch_bounds__(1024) qk_weight_sum_kernel(const float *partia
     part[x][y] = s.s;
     rest[x][y] = s.e;
     __syncthreads();
-    TwoSum t{part[y][x], rest[y][x]};
+    const int channel = threadIdx.x / 32, lane = threadIdx.x % 32, to = blockIdx.x * kSumChannels + channel;
+    TwoSum t{part[channel][lane], rest[channel][lane]};
     for (int o = 16; o > 0; o /= 2) t.add(__shfl_down_sync(0xffffffffu, t.s, o), __shfl_down_sync(0xffffffffu, t.e, o));
-    if (x == 0 && blockIdx.x * 32 + y < d) dst[blockIdx.x * 32 + y] = t.value();
+    if (lane == 0 && to < d) dst[to] = t.value();
 }
 
 template <typename T, bool VEC, int ROT, int LANES_>
@@ -488,7 +496,8 @@ cudaError_t launch_qk_norm_backward(const lq_qk_norm_config &c, const lq_qk_norm
         if (e != cudaSuccess) return e;
     }
     if (!sums) return cudaSuccess;
-    qk_weight_sum_kernel<<<dim3((unsigned)((c.d + 31) / 32), 2), 1024, 0, s>>>(partials, (int)grid, c.d, gwq, gwk);
+    qk_weight_sum_kernel<<<dim3((unsigned)((c.d + kSumChannels - 1) / kSumChannels), 2), 32 * kSumChannels, 0, s>>>(
+        partials, (int)grid, c.d, gwq, gwk);
     return cudaGetLastError();
 }
 

@@ -66,12 +66,12 @@ def test_weight_gradients_do_not_lose_more_with_the_rounds(heads, rounds):
     """Rows of ones and one gradient everywhere: dw = M heads g.  A thread takes heads x rounds rows, and for this g
     plain FP32 additions round with one sign, up to 0.5 u of each partial sum: n of them leave up to
     sum_i 0.5 u i / n = 0.25 (n + 1) u, the same in every thread.  Allowed: that of 32 rows, or of one token's heads,
-    and the roundings of the thread's sum, of the CTA's and of the result, 1.5 u."""
+    that of the CTA's 8 rows of threads, and the roundings of both sums and of the result, 1.5 u."""
     M, d, g = rounds * 8192, 256, float.fromhex("0x1.f08ccp+0")
     x, dy, w = torch.ones(M, heads, d, device=DEV), torch.full((M, heads, d), g, device=DEV), torch.ones(d, device=DEV)
     gw = lq.qk_norm_rotate_backward(dy, None, x, norm="rms", eps=1e-30, weight_q=w)[2]
     off = (gw.double().cpu() / (M * heads * g) - 1).abs().max()
-    assert off <= (0.25 * (max(32, heads) + 1) + 1.5) * plain_ops.U, float(off) / plain_ops.U
+    assert off <= (0.25 * (max(32, heads) + 1 + 8 + 1) + 1.5) * plain_ops.U, float(off) / plain_ops.U
 
 
 @pytest.mark.parametrize("M,hq,hk,d,rot,pairs", [(8192 + 5, 1, 1, 256, 256, "half"), (16384 + 3, 1, 2, 128, 128, "half"),
@@ -81,7 +81,7 @@ def test_weight_gradients_do_not_lose_more_with_the_rounds(heads, rounds):
 def test_more_tokens_than_one_round_of_the_backward_kernel(M, hq, hk, d, rot, pairs, dtype):
     """The grid is capped at 1024 CTAs (1024 x 8, 16 or 32 rows): threads carry their weight gradients over rounds,
     the last of which is partly dead.  dw is held to the additions that are made: a thread's rows, one by one, and
-    three roundings of larger sums: (48 + at most 9) u of the sum of absolute values, 3.4e-6.  One row's part is
+    32 more of the CTA's, and three roundings of larger sums: (48 + at most 41) u of the sum of absolute values, 5.3e-6.  One row's part is
     1 / (M heads) of that sum, 7.6e-6 and more."""
     gen = torch.Generator().manual_seed(M)
     on = lambda *s: torch.randn(*s, generator=gen).to(dtype).to(DEV)  # noqa: E731
@@ -108,4 +108,4 @@ def test_more_tokens_than_one_round_of_the_backward_kernel(M, hq, hk, d, rot, pa
         plain_ops.check(got[i], want["dx"], dtype, "dx")
         value, loose = want["dw"]
         C = 2 * plain_ops.C_QK
-        plain_ops.check(got[2 + i], (value, loose * (C + rounds * heads + 3) / (C + M * heads)), F32, "dw")
+        plain_ops.check(got[2 + i], (value, loose * (C + rounds * heads + 32 + 3) / (C + M * heads)), F32, "dw")
